@@ -3,7 +3,21 @@
 The compute path is the C-ABI library ``libtide.so`` (hand-written HIP kernels); this package only
 marshals arguments to it.  Importing the package does not load the library; the first call does,
 and fails loudly if it has not been built (``python -m all_gather_placement_amd.build``).
+
+``libtide_step.so`` holds the training-step operators on either side of the collectives (gradient norm
+and clipping, layer norm, embedding, with their gradients); they are bound in :mod:`.step`.
 """
+from .step import (  # noqa: F401
+    clip_grad_norm,
+    embedding,
+    embedding_bwd,
+    grad_clip,
+    grad_norm,
+    layer_norm,
+    layer_norm_bwd,
+    load_step_library,
+    step_library_path,
+)
 from .tide import (  # noqa: F401
     TIDE_AG_COPY2D,
     TIDE_AG_KERNEL,

@@ -1,4 +1,4 @@
-"""Build libtide.so (C ABI + gfx950 kernels) and libtide_probe.so in-tree with hipcc.
+"""Build libtide.so (C ABI + gfx950 kernels), libtide_step.so and libtide_probe.so in-tree with hipcc.
 
     python -m all_gather_placement_amd.build
 
@@ -7,7 +7,8 @@ The libraries are compiled for gfx950 only.  Packed-fp32 instructions are disabl
 used, so fp32 denormals and rounding are IEEE.
 
 Each library embeds a build id: the first 16 hex digits of the SHA-256 of its sources, the headers
-they include and the compile flags (``tide_build_id()`` / ``tide_probe_build_id()``).
+they include and the compile flags (``tide_build_id()`` / ``tide_step_build_id()`` /
+``tide_probe_build_id()``).
 :func:`ensure_built` rebuilds a library whose embedded id differs from the sources in the tree, and
 the bindings refuse to load one, so a library built from other sources is never run.
 """
@@ -28,6 +29,8 @@ LIB = os.path.join(PKG, "libtide.so")
 SOURCES = ["layout.cpp", "api.cpp", "kernels.hip"]
 PROBE_LIB = os.path.join(PKG, "libtide_probe.so")
 PROBE_SOURCES = ["probe.hip"]
+STEP_LIB = os.path.join(PKG, "libtide_step.so")
+STEP_SOURCES = ["step_api.cpp", "step_norm.hip", "step_layer_norm.hip", "step_embedding.hip"]
 ARCH = "gfx950"
 
 # Everything each library is compiled from (its sources and every header they include).
@@ -36,8 +39,10 @@ HASHED = {
          + [os.path.join(INCLUDE, "tide.h")],
     PROBE_LIB: [os.path.join(CSRC, f) for f in ("probe.hip", "tide_internal.h")]
                + [os.path.join(INCLUDE, "tide_probe.h")],
+    STEP_LIB: [os.path.join(CSRC, f) for f in (*STEP_SOURCES, "step_internal.h", "step_device.h")]
+              + [os.path.join(INCLUDE, f) for f in ("tide_step.h", "tide.h")],
 }
-ID_SYMBOL = {LIB: "tide_build_id", PROBE_LIB: "tide_probe_build_id"}
+ID_SYMBOL = {LIB: "tide_build_id", PROBE_LIB: "tide_probe_build_id", STEP_LIB: "tide_step_build_id"}
 
 
 def hipcc() -> str:
@@ -100,9 +105,10 @@ def check_current(lib: str = LIB, loaded=None) -> None:
 
 
 def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, probe: bool = True) -> str:
-    """Compile every source and link the shared library (and the probe library); returns its path."""
+    """Compile every source and link the shared library (and the step and probe libraries); returns its path."""
     if probe and out == LIB:
         build(verbose=verbose, extra=extra, out=PROBE_LIB, sources=PROBE_SOURCES, probe=False)
+        build(verbose=verbose, extra=extra, out=STEP_LIB, sources=STEP_SOURCES, probe=False)
     objdir = os.path.join(PKG, "_build", os.path.splitext(os.path.basename(out))[0])
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
@@ -110,14 +116,20 @@ def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, prob
     bid = source_hash(key, extra)
     id_flag = [f"-DTIDE_BUILD_ID=\"{bid}\""]
     objs = []
+    running = []
     for src in sources:
         obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = [cc, *compile_flags(extra), *id_flag, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        running.append(subprocess.Popen(cmd))
         objs.append(obj)
+    for p in running:  # all of them end before an error is raised
+        p.wait()
+    for p in running:
+        if p.returncode != 0:
+            raise subprocess.CalledProcessError(p.returncode, p.args)
     tmp = out + ".tmp"
     link = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp,
             "-Wl,-rpath,/opt/rocm/lib", "-L/opt/rocm/lib", "-lamdhip64"]
@@ -144,7 +156,7 @@ def is_current(lib: str) -> bool:
 def ensure_built(verbose: bool = False) -> str:
     """Build the libraries if they are missing or were built from other sources (tests, smoke and
     benchmark entry points); returns the path of libtide.so."""
-    if not (is_current(LIB) and is_current(PROBE_LIB)):
+    if not (is_current(LIB) and is_current(PROBE_LIB) and is_current(STEP_LIB)):
         build(verbose=verbose)
     return LIB
 

@@ -1,0 +1,128 @@
+// Declarations shared by the entry points and the kernels of libtide_step.so.
+#pragma once
+
+#include <stdint.h>
+
+#include "../../include/tide_step.h"
+
+namespace tide_step {
+
+// ---------------------------------------------------------------------------------------------
+// Gradient norm and clipping
+// ---------------------------------------------------------------------------------------------
+
+// A tensor is cut into chunks of 16 KiB, four 16-byte vectors for each of 256 threads; the last
+// chunk of a tensor holds what is left.  A launch walks the chunks of up to kNormBatch tensors in
+// order, workgroup b taking b, b + grid, ...  Tensors are named in the kernel's arguments (4 KiB),
+// so a call needs no device table, copy or event.
+constexpr int kNormThreads = 256;
+constexpr int kNormChunkBytes = 16384;
+constexpr int kNormMaxWgs = 2048;
+constexpr int64_t kMaxNormElems = int64_t(1) << 42;
+constexpr int norm_chunk_elems(int dtype) { return kNormChunkBytes / (dtype == TIDE_BF16 ? 2 : 4); }
+
+struct NormEntry {
+  const void* p;
+  uint32_t first;  // chunk of the launch that the tensor begins with
+  uint32_t last;   // elements of the tensor's last chunk
+};
+constexpr int kNormBatch = 250;
+struct NormTable {
+  int32_t count;
+  uint32_t chunks;
+  NormEntry e[kNormBatch];
+};
+static_assert(sizeof(NormTable) <= 4032, "kernel arguments stay within 4 KiB");
+
+struct ClipEntry {
+  const void* p;
+  void* out;
+  uint32_t first;
+  uint32_t last;
+};
+constexpr int kClipBatch = 160;
+struct ClipTable {
+  int32_t count;
+  uint32_t chunks;
+  ClipEntry e[kClipBatch];
+};
+static_assert(sizeof(ClipTable) <= 4032, "kernel arguments stay within 4 KiB");
+
+// Each returns a hipError_t.
+int launch_norm_partial(const NormTable& t, int dtype, double* partial, int grid, void* stream);
+int launch_norm_finish(const double* partial, int n, double* sumsq, float* norm, void* stream);
+int launch_clip(const ClipTable& t, int dtype, const double* sumsq, double max_norm, float* norm, int grid,
+                void* stream);
+
+// ---------------------------------------------------------------------------------------------
+// Layer norm
+// ---------------------------------------------------------------------------------------------
+
+struct LayerNormArgs {
+  int64_t rows, cols;
+  const void* x;
+  int64_t x_stride;
+  const void* weight;
+  const void* bias;
+  float eps;
+  void* y;
+  int64_t y_stride;
+  float* mean;
+  float* rstd;
+};
+int launch_layer_norm(const LayerNormArgs& a, int dtype, int param_dtype, void* stream);
+
+struct LayerNormBwdArgs {
+  int64_t rows, cols;
+  const void* dy;
+  int64_t dy_stride;
+  const void* x;
+  int64_t x_stride;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  int64_t dx_stride;
+  void* dweight;
+  void* dbias;
+  float* partial;  // [groups][2][cols]: each workgroup's sums over its rows
+};
+// Workgroups of the gradient's first kernel, each leaving a partial sum of every column.
+int layer_norm_bwd_groups(int64_t rows, int64_t cols, int dtype);
+int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, int param_dtype, void* stream);
+
+// ---------------------------------------------------------------------------------------------
+// Embedding
+// ---------------------------------------------------------------------------------------------
+
+int launch_embedding(int64_t tokens, const void* ids, int ids_dtype, int64_t vocab, int64_t dim, const void* table,
+                     int dtype, float scale, void* out, void* stream);
+
+// The gradient's sort gives each workgroup a range of table rows; it finds the range's tokens by
+// reading all ids.  A range holds at most kSortMaxRows rows, and there are kSortRanges ranges (one
+// for each compute unit) where the table has that many rows.
+constexpr int kSortMaxRows = 512;
+constexpr int kSortRanges = 256;
+inline int64_t sort_rows(int64_t vocab) {
+  const int64_t r = (vocab + kSortRanges - 1) / kSortRanges;
+  return r < 1 ? 1 : (r > kSortMaxRows ? kSortMaxRows : r);
+}
+// Sorted tokens are summed in pieces of kPiece.  A run of equal ids that crosses a border of pieces
+// leaves fp32 partial sums, at most two for each piece, that a second kernel adds in order.
+constexpr int kPiece = 32;
+
+struct EmbeddingBwdArgs {
+  int64_t tokens, vocab, dim;
+  const void* ids;
+  const void* dy;
+  float scale;
+  bool accumulate;
+  void* dtable;
+  int32_t* sorted_token;  // [tokens]
+  int32_t* sorted_row;    // [tokens]
+  int32_t* num_sorted;    // tokens inside the table
+  float* partial;         // [pieces][2][dim]
+};
+int launch_embedding_bwd(const EmbeddingBwdArgs& a, int dtype, int ids_dtype, void* stream);
+
+}  // namespace tide_step
