@@ -269,7 +269,7 @@ bool vector_ok(const void* p, int dtype) { return aligned(p, size_of(dtype)); }
 inline Range opt_range(const void* p, int64_t bytes) { return p == nullptr ? Range{0, 0} : range_of(p, bytes); }
 
 int64_t layer_norm_bwd_bytes(int64_t rows, int64_t cols, int dtype) {
-  return (int64_t(layer_norm_bwd_groups(rows, cols, dtype)) * 2 * cols * 4 + 15) / 16 * 16;
+  return int64_t(layer_norm_bwd_groups(rows, cols, dtype)) * 2 * layer_norm_bwd_padded(cols) * 4;
 }
 
 }  // namespace

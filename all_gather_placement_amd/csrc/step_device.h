@@ -1,4 +1,4 @@
-// Device helpers shared by the step kernels: vectors of eight elements, conversions, reductions.
+// Device helpers shared by the step kernels: vectors of elements, conversions, reductions.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -8,18 +8,31 @@
 namespace tide_step {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned short bf16_t;  // bit pattern
 
-// 16 bytes at any element boundary: gfx950 reads and writes unaligned vectors in one instruction.
-struct __attribute__((packed, aligned(2))) Any16 {
-  u32x4 v;
-};
+// 16 and 8 bytes at any element boundary: gfx950 reads and writes unaligned vectors in one instruction.
+// kOnce marks what is read or written once (non-temporal): it does not push out what is used again.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+#define TIDE_STEP_GLOBAL __attribute__((address_space(1)))
+template <bool kOnce = false>
 __device__ __forceinline__ u32x4 load16(const void* p) {
-  return reinterpret_cast<const __attribute__((address_space(1))) Any16*>((uintptr_t)p)->v;
+  const TIDE_STEP_GLOBAL u32x4_any* g = reinterpret_cast<const TIDE_STEP_GLOBAL u32x4_any*>((uintptr_t)p);
+  if constexpr (kOnce) return __builtin_nontemporal_load(g);
+  return *g;
 }
+template <bool kOnce = false>
 __device__ __forceinline__ void store16(void* p, u32x4 v) {
-  reinterpret_cast<__attribute__((address_space(1))) Any16*>((uintptr_t)p)->v = v;
+  TIDE_STEP_GLOBAL u32x4_any* g = reinterpret_cast<TIDE_STEP_GLOBAL u32x4_any*>((uintptr_t)p);
+  if constexpr (kOnce)
+    __builtin_nontemporal_store(v, g);
+  else
+    *g = v;
+}
+__device__ __forceinline__ u32x2 load8(const void* p) {
+  return *reinterpret_cast<const TIDE_STEP_GLOBAL u32x2_any*>((uintptr_t)p);
 }
 
 __device__ __forceinline__ float widen(bf16_t b) { return __uint_as_float(static_cast<unsigned int>(b) << 16); }
@@ -40,75 +53,104 @@ __device__ __forceinline__ bf16_t narrow<bf16_t>(float f) {
   return __builtin_bit_cast(unsigned short, static_cast<__bf16>(f));
 }
 
-// Eight neighbouring elements as they lie in memory.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<bf16_t> {
-  u32x4 v;
+// E neighbouring elements as they lie in memory: 8, 16 or 32 bytes.
+template <typename T, int E>
+struct Raw {
+  static constexpr int kWords = E * int(sizeof(T)) / 4;
+  unsigned int w[kWords];
   __device__ __forceinline__ float get(int i) const {
-    const unsigned int w = v[i >> 1];
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    if constexpr (sizeof(T) == 2) {
+      const unsigned int u = w[i >> 1];
+      return __uint_as_float((i & 1) ? (u & 0xffff0000u) : (u << 16));
+    } else {
+      return __uint_as_float(w[i]);
+    }
+  }
+  // Keeps the compiler from holding values made of this vector (twice the registers for bf16) until
+  // they are used again: beyond this point they are made again.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) asm volatile("" : "+v"(w[q]));
   }
 };
-template <>
-struct Raw8<float> {
-  u32x4 v[2];
-  __device__ __forceinline__ float get(int i) const { return __uint_as_float(v[i >> 2][i & 3]); }
-};
 
-// The first n (of 8) elements at p, zeros beyond; n <= 0 reads nothing.
-__device__ __forceinline__ Raw8<bf16_t> load8(const bf16_t* p, int n) {
-  Raw8<bf16_t> r;
-  if (n >= 8) {
-    r.v = load16(p);
-  } else {
-    r.v = u32x4{0, 0, 0, 0};
+// The first n (of E) elements at p, zeros beyond; n <= 0 reads nothing.
+template <typename T, int E, bool kOnce = false>
+__device__ __forceinline__ Raw<T, E> load_vec(const T* p, int n) {
+  Raw<T, E> r;
+  if (n >= E) {
+    if constexpr (r.kWords == 2) {
+      const u32x2 v = load8(p);
+      r.w[0] = v[0];
+      r.w[1] = v[1];
+    } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.v[i >> 1] |= static_cast<unsigned int>(p[i]) << (16 * (i & 1));
+      for (int q = 0; q < r.kWords / 4; ++q) {
+        const u32x4 v = load16<kOnce>(reinterpret_cast<const char*>(p) + 16 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r.w[4 * q + k] = v[k];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < r.kWords; ++q) r.w[q] = 0;
+#pragma unroll
+    for (int i = 0; i < E - 1; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          r.w[i >> 1] |= static_cast<unsigned int>(p[i]) << (16 * (i & 1));
+        else
+          r.w[i] = __float_as_uint(p[i]);
+      }
   }
   return r;
 }
-__device__ __forceinline__ Raw8<float> load8(const float* p, int n) {
-  Raw8<float> r;
-  if (n >= 8) {
-    r.v[0] = load16(p);
-    r.v[1] = load16(p + 4);
-  } else {
-    r.v[0] = r.v[1] = u32x4{0, 0, 0, 0};
+// The first n (of E) values of f to p, rounded.
+template <typename T, int E, bool kOnce = false>
+__device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[E]) {
+  if (n >= E) {
+    unsigned int w[Raw<T, E>::kWords];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.v[i >> 2][i & 3] = __float_as_uint(p[i]);
-  }
-  return r;
-}
-__device__ __forceinline__ void store8(bf16_t* p, int n, const float f[8]) {
-  if (n >= 8) {
-    store16(p, u32x4{round_bf16x2(f[0], f[1]), round_bf16x2(f[2], f[3]), round_bf16x2(f[4], f[5]),
-                     round_bf16x2(f[6], f[7])});
-  } else {
+    for (int q = 0; q < Raw<T, E>::kWords; ++q) {
+      if constexpr (sizeof(T) == 2)
+        w[q] = round_bf16x2(f[2 * q], f[2 * q + 1]);
+      else
+        w[q] = __float_as_uint(f[q]);
+    }
+    static_assert(Raw<T, E>::kWords % 4 == 0, "stores are of 16 bytes");
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = narrow<bf16_t>(f[i]);
-  }
-}
-__device__ __forceinline__ void store8(float* p, int n, const float f[8]) {
-  if (n >= 8) {
-    store16(p, __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]}));
-    store16(p + 4, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
+    for (int q = 0; q < Raw<T, E>::kWords / 4; ++q)
+      store16<kOnce>(reinterpret_cast<char*>(p) + 16 * q, u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]});
   } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = f[i];
+    for (int i = 0; i < E - 1; ++i)
+      if (i < n) p[i] = narrow<T>(f[i]);
   }
 }
+// Elements of a 16-byte vector.
+template <typename T>
+constexpr int kVec = 16 / int(sizeof(T));
 
+// One step of a sum within rows of 16 lanes, on the VALU (no LDS traffic).
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+}
 // Sum over aligned groups of L lanes (a power of two up to 64), the same in every lane of a group.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m, 64);
+  if constexpr (L >= 2) v = dpp_add<0xb1>(v);   // lane ^ 1
+  if constexpr (L >= 4) v = dpp_add<0x4e>(v);   // lane ^ 2
+  if constexpr (L >= 8) v = dpp_add<0x141>(v);  // mirrored within 8: the other quad
+  if constexpr (L >= 16) v = dpp_add<0x140>(v); // mirrored within 16: the other half
+  if constexpr (L >= 32) {  // rows 0 and 1, 2 and 3
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L >= 64) {  // the halves of the wave
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
 __device__ __forceinline__ double wave_sum(double v) {

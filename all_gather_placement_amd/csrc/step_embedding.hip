@@ -40,11 +40,11 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(int64_t tokens, con
     const int64_t id = ids[t];
     float f[8] = {};
     if (id >= 0 && id < vocab) {
-      const Raw8<T> r = load8(table + id * dim + c, n);
+      const Raw<T, 8> r = load_vec<T, 8>(table + id * dim + c, n);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = r.get(k) * scale;
     }
-    store8(out + t * dim + c, n, f);
+    store_vec<T, 8>(out + t * dim + c, n, f);
   }
 }
 
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   for (int r = wave; r < rows; r += kSortWaves) {
     if (!empty[r]) continue;
     T* out = static_cast<T*>(a.dtable) + (r0 + r) * a.dim;
-    for (int64_t c = lane * 8; c < a.dim; c += 512) store8(out + c, int(a.dim - c < 8 ? a.dim - c : 8), zero);
+    for (int64_t c = lane * 8; c < a.dim; c += 512) store_vec<T, 8>(out + c, int(a.dim - c < 8 ? a.dim - c : 8), zero);
   }
 }
 
@@ -161,17 +161,17 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
 // ---------------------------------------------------------------------------------------------
 
 template <typename T>
-__device__ __forceinline__ void write_row(const EmbeddingBwdArgs& a, int row, int64_t c, int n, const float acc[8]) {
+__device__ __forceinline__ void write_row(const EmbeddingBwdArgs& a, int row, int64_t c, int n, const float (&acc)[8]) {
   T* out = static_cast<T*>(a.dtable) + int64_t(row) * a.dim + c;
   float f[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] = acc[k] * a.scale;
   if (a.accumulate) {
-    const Raw8<T> old = load8(out, n);
+    const Raw<T, 8> old = load_vec<T, 8>(out, n);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] += old.get(k);
   }
-  store8(out, n, f);
+  store_vec<T, 8>(out, n, f);
 }
 
 // blockIdx.x: piece of kPiece sorted tokens; a wave takes 512 columns of it.
@@ -190,13 +190,13 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArg
     int row = a.sorted_row[begin];
     bool open = row == before;  // the run began in an earlier piece
     for (int i = begin; i < end; ++i) {
-      const Raw8<T> r = load8(static_cast<const T*>(a.dy) + int64_t(a.sorted_token[i]) * a.dim + c, n);
+      const Raw<T, 8> r = load_vec<T, 8>(static_cast<const T*>(a.dy) + int64_t(a.sorted_token[i]) * a.dim + c, n);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] += r.get(k);
       const int next = i + 1 < end ? a.sorted_row[i + 1] : after;
       if (next == row && i + 1 < end) continue;
       if (open || next == row)
-        store8(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
+        store_vec<float, 8>(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
       else
         write_row<T>(a, row, c, n, acc);
 #pragma unroll
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdAr
     const int n = int(a.dim - c < 8 ? a.dim - c : 8);
     float acc[8] = {};
     for (int64_t q = piece; q <= last; ++q) {
-      const Raw8<float> r = load8(a.partial + (2 * q + (q == piece ? 1 : 0)) * a.dim + c, n);
+      const Raw<float, 8> r = load_vec<float, 8>(a.partial + (2 * q + (q == piece ? 1 : 0)) * a.dim + c, n);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] += r.get(k);
     }

@@ -85,10 +85,12 @@ struct LayerNormBwdArgs {
   int64_t dx_stride;
   void* dweight;
   void* dbias;
-  float* partial;  // [groups][2][cols]: each workgroup's sums over its rows
+  float* partial;  // [groups][2][layer_norm_bwd_padded(cols)]: each workgroup's sums over its rows
 };
 // Workgroups of the gradient's first kernel, each leaving a partial sum of every column.
 int layer_norm_bwd_groups(int64_t rows, int64_t cols, int dtype);
+// Columns of a partial sum: up to whole 16-byte vectors.
+constexpr int64_t layer_norm_bwd_padded(int64_t cols) { return (cols + 3) / 4 * 4; }
 int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, int param_dtype, void* stream);
 
 // ---------------------------------------------------------------------------------------------

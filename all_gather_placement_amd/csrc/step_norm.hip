@@ -43,16 +43,8 @@ __device__ __forceinline__ int entry_of(const Table& t, uint32_t c) {
 template <typename T>
 constexpr int kChunk = kNormChunkBytes / int(sizeof(T));
 template <typename T>
-constexpr int kVec = 16 / int(sizeof(T));  // elements of a 16-byte vector
-
-template <typename T>
 __device__ __forceinline__ float lane_of(u32x4 v, int i) {
-  if constexpr (sizeof(T) == 2) {
-    const unsigned int w = v[i >> 1];
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
-  } else {
-    return __uint_as_float(v[i]);
-  }
+  return Raw<T, kVec<T>>{v[0], v[1], v[2], v[3]}.get(i);
 }
 
 template <typename T>
