@@ -6,12 +6,12 @@
 // HBM bounds the lookup: rows are read and written once in 16-byte vectors.
 //
 // The gradient has to write every row of the table, and most rows have no token.  Its first kernel
-// brings tokens of equal id together and writes the zero rows meanwhile.  Each workgroup owns a
-// range of rows.  It reads all ids (which stay in the L2), counts those of each of its rows and
-// those below its range -- the place where its tokens begin -- and then places its tokens in
-// ascending order: a stable counting sort with no traffic between workgroups.  The second kernel
-// sums the sorted tokens in pieces of equal length, so a frequent id is shared by many waves, and a
-// third adds the partial sums of ids that cross pieces, in order.
+// brings tokens of equal id together.  Workgroup b of 2^k owns the rows v with v mod 2^k = b, so that
+// low, frequent ids are shared evenly.  It reads all ids (which stay in the L2), counts those of each of
+// its rows and those of lower workgroups -- the place where its tokens begin -- and then places its
+// tokens in ascending order: a stable counting sort with no traffic between workgroups.  The second kernel sums the sorted tokens in pieces of equal length, so a frequent
+// id is shared by many waves, and writes the rows of zeros beside that.  A third adds the partial sums
+// of ids that cross pieces, in a fixed order.
 #include "step_device.h"
 #include "step_internal.h"
 
@@ -19,6 +19,15 @@ namespace tide_step {
 namespace {
 
 constexpr int kThreads = 256;
+
+// Workgroups for n items, `per` each: a launch holds less than 2^32 threads, so kernels go on to the
+// items a grid further.
+constexpr int64_t kMaxGrid = int64_t(1) << 21;
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline unsigned grid_of(int64_t n, int64_t per) {
+  const int64_t g = ceil_div(n, per);
+  return unsigned(g < kMaxGrid ? g : kMaxGrid);
+}
 
 // ---------------------------------------------------------------------------------------------
 // Lookup
@@ -45,24 +54,25 @@ __global__ __launch_bounds__(kThreads) void embedding_rows_kernel(int64_t tokens
                                                                   T* __restrict__ out, int wshift) {
   constexpr int E = kVec<T>;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t t = (int64_t(blockIdx.x) << (2 - wshift)) + (wave >> wshift);
-  if (t >= tokens) return;
-  const int64_t id = ids[t];
-  const bool inside = id >= 0 && id < vocab;
-  const T* row = table + (inside ? id * dim : 0);
-  T* o = out + t * dim;
   const int64_t step = int64_t(64 * NV * E) << wshift;
-  for (int64_t c0 = int64_t(wave & ((1 << wshift) - 1)) * (64 * NV * E); c0 < dim; c0 += step) {
-    Raw<T, E> r[NV];
+  for (int64_t t = (int64_t(blockIdx.x) << (2 - wshift)) + (wave >> wshift); t < tokens;
+       t += int64_t(gridDim.x) << (2 - wshift)) {
+    const int64_t id = ids[t];
+    const bool inside = id >= 0 && id < vocab;
+    const T* row = table + (inside ? id * dim : 0);
+    T* o = out + t * dim;
+    for (int64_t c0 = int64_t(wave & ((1 << wshift) - 1)) * (64 * NV * E); c0 < dim; c0 += step) {
+      Raw<T, E> r[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = c0 + (v * 64 + lane) * E;
-      r[v] = load_vec<T, E>(row + c, inside ? tail<E>(dim - c) : 0);
-    }
+      for (int v = 0; v < NV; ++v) {
+        const int64_t c = c0 + (v * 64 + lane) * E;
+        r[v] = load_vec<T, E>(row + c, inside ? tail<E>(dim - c) : 0);
+      }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = c0 + (v * 64 + lane) * E;
-      if (c < dim) store_scaled<T, E>(o + c, tail<E>(dim - c), r[v], inside, scale);
+      for (int v = 0; v < NV; ++v) {
+        const int64_t c = c0 + (v * 64 + lane) * E;
+        if (c < dim) store_scaled<T, E>(o + c, tail<E>(dim - c), r[v], inside, scale);
+      }
     }
   }
 }
@@ -75,21 +85,23 @@ __global__ __launch_bounds__(kThreads) void embedding_narrow_kernel(int64_t toke
                                                                     T* __restrict__ out, int lshift) {
   constexpr int E = kVec<T>;
   const int groups = kThreads >> lshift, c = (threadIdx.x & ((1 << lshift) - 1)) * E;
-  const int64_t t0 = int64_t(blockIdx.x) * groups * NT + (threadIdx.x >> lshift);
-  int64_t id[NT];
+  for (int64_t t0 = int64_t(blockIdx.x) * groups * NT + (threadIdx.x >> lshift); t0 < tokens;
+       t0 += int64_t(gridDim.x) * groups * NT) {
+    int64_t id[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) id[i] = t0 + i * groups < tokens ? int64_t(ids[t0 + i * groups]) : -1;
-  Raw<T, E> r[NT];
+    for (int i = 0; i < NT; ++i) id[i] = t0 + i * groups < tokens ? int64_t(ids[t0 + i * groups]) : -1;
+    Raw<T, E> r[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const bool inside = id[i] >= 0 && id[i] < vocab;
-    r[i] = load_vec<T, E>(table + (inside ? id[i] * dim : 0) + c, inside ? dim - c : 0);
-  }
+    for (int i = 0; i < NT; ++i) {
+      const bool inside = id[i] >= 0 && id[i] < vocab;
+      r[i] = load_vec<T, E>(table + (inside ? id[i] * dim : 0) + c, inside ? dim - c : 0);
+    }
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t t = t0 + i * groups;
-    if (t < tokens && c < dim)
-      store_scaled<T, E>(out + t * dim + c, dim - c, r[i], id[i] >= 0 && id[i] < vocab, scale);
+    for (int i = 0; i < NT; ++i) {
+      const int64_t t = t0 + i * groups;
+      if (t < tokens && c < dim)
+        store_scaled<T, E>(out + t * dim + c, dim - c, r[i], id[i] >= 0 && id[i] < vocab, scale);
+    }
   }
 }
 
@@ -99,6 +111,15 @@ __global__ __launch_bounds__(kThreads) void embedding_narrow_kernel(int64_t toke
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
+
+// Id k of a 16-byte vector.
+template <typename I>
+__device__ __forceinline__ int64_t id_of(u32x4 v, int k) {
+  if constexpr (sizeof(I) == 4)
+    return int(v[k]);
+  else
+    return int64_t(uint64_t(v[2 * k]) | uint64_t(v[2 * k + 1]) << 32);
+}
 
 // Inclusive sum over the wave.
 __device__ __forceinline__ int wave_scan(int v) {
@@ -127,77 +148,124 @@ __device__ __forceinline__ int block_exclusive(int v, int* lds, int* total) {
   return before + incl - v;
 }
 
+// The lanes whose `row` equals this lane's, of those in `active`.  A range seldom has more than two
+// different rows among 64 tokens: the first few are taken one by one, what is left by the rows' bits.
+__device__ __forceinline__ uint64_t same_row(int row, uint64_t active, int bits, int lane) {
+  uint64_t same = 0, todo = active;
+  for (int k = 0; k < 3 && todo != 0; ++k) {
+    const int r = __builtin_amdgcn_readlane(row, __ffsll((unsigned long long)todo) - 1);
+    const uint64_t of_r = __ballot(row == r) & todo;
+    if (row == r) same = of_r;
+    todo &= ~of_r;
+  }
+  if (todo != 0) {
+    uint64_t rest = todo;
+    for (int k = 0; k < bits; ++k) {
+      const uint64_t set = __ballot((row >> k) & 1);
+      rest &= (row >> k) & 1 ? set : ~set;
+    }
+    if ((todo >> lane) & 1) same = rest;
+  }
+  return same;
+}
+
+// Workgroups below `ranges` sort; the others write zeros to the table, one 16-byte store a thread:
+// short-lived workgroups in order of address write fastest (131072 x 4096 bf16 with 1024 threads 169 us,
+// a wave for each row 194).  Rows that have tokens are written again by the sums, which costs less than
+// waiting for the sort and asking for each row whether it has any (237 us with the sums, 30 more than
+// they take one after the other).
 template <typename T, typename I>
-__global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingBwdArgs a, int rows_per_range) {
-  extern __shared__ int count[];  // [kSortWaves][rows_per_range]: tokens of a wave's part, then their places
+__global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingBwdArgs a, unsigned ranges, int shift,
+                                                                      int most_rows, int bits) {
+  if (blockIdx.x >= ranges) {
+    constexpr int N = kVec<T>;
+    const float none[N] = {};
+    const int64_t end = a.vocab * a.dim;
+    for (int64_t e = (int64_t(blockIdx.x - ranges) * kSortThreads + threadIdx.x) * N; e < end;
+         e += int64_t(gridDim.x - ranges) * kSortThreads * N)
+      store_vec<T, N>(static_cast<T*>(a.dtable) + e, tail<N>(end - e), none);
+    return;
+  }
+  extern __shared__ int count[];  // [kSortWaves][most_rows]: tokens of a wave's part, then their places
   __shared__ int lds[kSortWaves];
+  constexpr int E = kVec<I>;
   const I* __restrict__ ids = static_cast<const I*>(a.ids);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t r0 = int64_t(blockIdx.x) * rows_per_range;
-  const int rows = int(a.vocab - r0 < rows_per_range ? a.vocab - r0 : rows_per_range);
-  for (int i = threadIdx.x; i < kSortWaves * rows_per_range; i += kSortThreads) count[i] = 0;
+  const unsigned vocab = unsigned(a.vocab), range = blockIdx.x, mask = (1u << shift) - 1;
+  const int rows = int((vocab - range + mask) >> shift);  // range, range + 2^shift, ...: at least one
+  for (int i = threadIdx.x; i < kSortWaves * most_rows; i += kSortThreads) count[i] = 0;
   __syncthreads();
 
   // each wave reads a part of the tokens of its own, in order
-  const int64_t part = ((a.tokens + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+  constexpr int kAhead = 8;  // loads in flight
+  const int64_t part = ceil_div(ceil_div(a.tokens, kSortWaves), 64 * E) * (64 * E);
   const int64_t begin = wave * part, end = begin + part < a.tokens ? begin + part : a.tokens;
-  int* mine = count + wave * rows_per_range;
+  int* mine = count + wave * most_rows;
   int below = 0;
-  for (int64_t t = begin + lane; t < end; t += 64) {
-    const int64_t id = ids[t];
-    below += id >= 0 && id < r0;
-    if (id >= r0 && id < r0 + rows) atomicAdd(mine + (id - r0), 1);
+  const auto see = [&](int64_t id) {
+    const bool inside = uint64_t(id) < vocab;
+    const unsigned r = unsigned(id) & mask;
+    below += inside && r < range;
+    if (inside && r == range) atomicAdd(mine + (unsigned(id) >> shift), 1);
+  };
+  int64_t t = begin;
+  for (; t + 64 * E * kAhead <= end; t += 64 * E * kAhead) {
+    u32x4 v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) v[j] = load16(ids + t + (j * 64 + lane) * E);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int k = 0; k < E; ++k) see(id_of<I>(v[j], k));
+  }
+  for (; t < end; t += 64 * kAhead) {
+    I v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) v[j] = t + j * 64 + lane < end ? ids[t + j * 64 + lane] : I(-1);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) see(v[j]);
   }
   int base;
   block_exclusive(below, lds, &base);  // its barriers also end the counting
 
-  // places: rows in order, a row's tokens by wave
+  // places: the range's rows in order, a row's tokens by wave
   int of_row = 0;
   if (int(threadIdx.x) < rows)
-    for (int w = 0; w < kSortWaves; ++w) of_row += count[w * rows_per_range + threadIdx.x];
+    for (int w = 0; w < kSortWaves; ++w) of_row += count[w * most_rows + threadIdx.x];
   int found;
   int place = base + block_exclusive(of_row, lds, &found);
   if (int(threadIdx.x) < rows)
     for (int w = 0; w < kSortWaves; ++w) {
-      const int n = count[w * rows_per_range + threadIdx.x];
-      count[w * rows_per_range + threadIdx.x] = place;
+      const int n = count[w * most_rows + threadIdx.x];
+      count[w * most_rows + threadIdx.x] = place;
       place += n;
     }
-  __shared__ unsigned char empty[kSortMaxRows];
-  if (int(threadIdx.x) < rows) empty[threadIdx.x] = of_row == 0;
-  if (r0 + rows == a.vocab && threadIdx.x == 0) *a.num_sorted = base + found;
+  if (range == ranges - 1 && threadIdx.x == 0) *a.num_sorted = base + found;
+  if (found == 0) return;
   __syncthreads();
 
-  if (found > 0) {
-    for (int64_t t0 = begin; t0 < end; t0 += 64) {
-      const int64_t t = t0 + lane;
-      const int64_t id = t < end ? int64_t(ids[t]) : -1;
-      const int row = id >= r0 && id < r0 + rows ? int(id - r0) : -1;
-      uint64_t todo = __ballot(row >= 0);
-      while (todo != 0) {
-        const int leader = __ffsll((unsigned long long)todo) - 1;
-        const int r = __shfl(row, leader, 64);
-        const uint64_t same = __ballot(row == r);
+  for (int64_t t0 = begin; t0 < end; t0 += 64 * kAhead) {
+    I v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) v[j] = t0 + j * 64 + lane < end ? ids[t0 + j * 64 + lane] : I(-1);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t id = v[j];
+      const bool here = uint64_t(id) < vocab && (unsigned(id) & mask) == range;
+      const uint64_t active = __ballot(here);
+      if (active == 0) continue;
+      const int row = here ? int(unsigned(id) >> shift) : 0;
+      const uint64_t same = same_row(row, active, bits, lane);
+      if (here) {
         // only this wave uses this place, and its LDS accesses stay in order
-        const int first = __hip_atomic_load(mine + r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        if (row == r) {
-          const int at = first + __popcll(same & ((uint64_t(1) << lane) - 1));
-          a.sorted_token[at] = int(t);
-          a.sorted_row[at] = int(r0) + r;
-        }
-        if (lane == leader)
-          __hip_atomic_store(mine + r, first + __popcll(same), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        todo &= ~same;
+        const int first = __hip_atomic_load(mine + row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        const int at = first + __popcll(same & ((uint64_t(1) << lane) - 1));
+        a.sorted_token[at] = int(t0 + j * 64 + lane);
+        a.sorted_row[at] = int(id);
+        if (lane == 63 - __clzll((long long)same))  // the last of its row: the next place
+          __hip_atomic_store(mine + row, at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
       }
     }
-  }
-
-  if (a.accumulate) return;
-  const float zero[8] = {};
-  for (int r = wave; r < rows; r += kSortWaves) {
-    if (!empty[r]) continue;
-    T* out = static_cast<T*>(a.dtable) + (r0 + r) * a.dim;
-    for (int64_t c = lane * 8; c < a.dim; c += 512) store_vec<T, 8>(out + c, int(a.dim - c < 8 ? a.dim - c : 8), zero);
   }
 }
 
@@ -205,99 +273,156 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
 // Gradient: sums
 // ---------------------------------------------------------------------------------------------
 
-template <typename T>
-__device__ __forceinline__ void write_row(const EmbeddingBwdArgs& a, int row, int64_t c, int n, const float (&acc)[8]) {
+template <typename T, int E>
+__device__ __forceinline__ void write_row(const EmbeddingBwdArgs& a, int row, int64_t c, int n, const float (&acc)[E]) {
   T* out = static_cast<T*>(a.dtable) + int64_t(row) * a.dim + c;
-  float f[8];
+  float f[E];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = acc[k] * a.scale;
+  for (int k = 0; k < E; ++k) f[k] = acc[k] * a.scale;
   if (a.accumulate) {
-    const Raw<T, 8> old = load_vec<T, 8>(out, n);
+    const Raw<T, E> old = load_vec<T, E>(out, n);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] += old.get(k);
+    for (int k = 0; k < E; ++k) f[k] += old.get(k);
   }
-  store_vec<T, 8>(out, n, f);
+  store_vec<T, E>(out, n, f);
 }
 
-// blockIdx.x: piece of kPiece sorted tokens; a wave takes 512 columns of it.
+// A wave's item: 64 vectors of columns of a piece of kPiece sorted tokens.  Eight rows of dy are in
+// flight at a time; they are added in order.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArgs a) {
-  const int64_t piece = blockIdx.x;
-  const int total = *a.num_sorted;
-  const int begin = int(piece * kPiece);
-  if (begin >= total) return;
-  const int end = begin + kPiece < total ? begin + kPiece : total;
-  const int before = begin > 0 ? a.sorted_row[begin - 1] : -1;
-  const int after = end < total ? a.sorted_row[end] : -1;
-  for (int64_t c = (int64_t(blockIdx.y) * kThreads + threadIdx.x) * 8; c < a.dim; c += int64_t(gridDim.y) * kThreads * 8) {
-    const int n = int(a.dim - c < 8 ? a.dim - c : 8);
-    float acc[8] = {};
-    int row = a.sorted_row[begin];
-    bool open = row == before;  // the run began in an earlier piece
-    for (int i = begin; i < end; ++i) {
-      const Raw<T, 8> r = load_vec<T, 8>(static_cast<const T*>(a.dy) + int64_t(a.sorted_token[i]) * a.dim + c, n);
+__device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t piece, int64_t c, int total) {
+  constexpr int E = kVec<T>, kAhead = 8;
+  const int lane = threadIdx.x & 63;
+  const int64_t begin = piece * kPiece;
+  const int cnt = int(total - begin < kPiece ? total - begin : kPiece);
+  // lane i holds token i of the piece; lanes kPiece and kPiece + 1 the rows after and before it
+  static_assert(kPiece + 2 <= 64, "a piece and its neighbours are held by one wave");
+  const int64_t at = lane < cnt ? begin + lane : lane == kPiece + 1 ? begin - 1 : lane == kPiece ? begin + cnt : -1;
+  const int rows = at >= 0 && at < total ? a.sorted_row[at] : -1;
+  const int tokens = lane < cnt ? a.sorted_token[at] : 0;
+  const int after = __builtin_amdgcn_readlane(rows, kPiece);
+  const int n = tail<E>(a.dim - c);
+  float acc[E] = {};
+  int row = __builtin_amdgcn_readlane(rows, 0);
+  bool open = row == __builtin_amdgcn_readlane(rows, kPiece + 1);  // the run began in an earlier piece
+  for (int i0 = 0; i0 < cnt; i0 += kAhead) {
+    Raw<T, E> r[kAhead];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += r.get(k);
-      const int next = i + 1 < end ? a.sorted_row[i + 1] : after;
-      if (next == row && i + 1 < end) continue;
-      if (open || next == row)
-        store_vec<float, 8>(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
-      else
-        write_row<T>(a, row, c, n, acc);
+    for (int j = 0; j < kAhead; ++j) {  // beyond the end the last token again, so that no branch parts the loads
+      const int64_t t = __builtin_amdgcn_readlane(tokens, i0 + j < cnt ? i0 + j : cnt - 1);
+      r[j] = load_vec<T, E, true>(static_cast<const T*>(a.dy) + t * a.dim + c, n);
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j;
+      if (i >= cnt) break;
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc[k] += r[j].get(k);
+      const int next = i + 1 < cnt ? __builtin_amdgcn_readlane(rows, i + 1) : after;
+      if (next == row && i + 1 < cnt) continue;
+      if (n > 0) {
+        if (open || next == row)
+          store_vec<float, E>(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
+        else
+          write_row<T, E>(a, row, c, n, acc);
+      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc[k] = 0.0f;
       row = next;
       open = false;
     }
   }
 }
 
-// blockIdx.x: piece that a run begins in and does not end in.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArgs a) {
+  constexpr int E = kVec<T>;
+  const int total = *a.num_sorted;
+  const int64_t chunks = ceil_div(a.dim, 64 * E), items = ceil_div(total, kPiece) * chunks;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  for (int64_t item = int64_t(blockIdx.x) * 4 + wave; item < items; item += int64_t(gridDim.x) * 4) {
+    const int64_t piece = item / chunks;
+    sum_piece<T>(a, piece, ((item - piece * chunks) * 64 + lane) * E, total);
+  }
+}
+
+// Adds the partial sums of a run that begins in a piece and ends in a later one: a workgroup takes 64
+// vectors of columns, its waves a quarter of the run's pieces each, in order; the quarters meet in LDS.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdArgs a) {
-  const int64_t piece = blockIdx.x;
+  constexpr int E = kVec<T>, kAhead = 8;
+  __shared__ float quarter[3][64 * E];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int total = *a.num_sorted;
-  const int64_t border = (piece + 1) * kPiece;
-  if (border >= total) return;
-  const int row = a.sorted_row[border];
-  if (a.sorted_row[border - 1] != row) return;
-  const int64_t begin = piece * kPiece;
-  if (begin > 0 && a.sorted_row[begin - 1] == row) return;  // begins earlier
-  // the last piece of the run: its tokens go on to before `hi`
-  int lo = int(border), hi = total;  // sorted_row[lo] == row, sorted_row[hi] != row
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (a.sorted_row[mid] == row)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int64_t last = lo / kPiece;
-  for (int64_t c = (int64_t(blockIdx.y) * kThreads + threadIdx.x) * 8; c < a.dim; c += int64_t(gridDim.y) * kThreads * 8) {
-    const int n = int(a.dim - c < 8 ? a.dim - c : 8);
-    float acc[8] = {};
-    for (int64_t q = piece; q <= last; ++q) {
-      const Raw<float, 8> r = load_vec<float, 8>(a.partial + (2 * q + (q == piece ? 1 : 0)) * a.dim + c, n);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += r.get(k);
+  const int64_t last_border = (int64_t(total) - 1) / kPiece;  // pieces 0 .. last_border hold tokens
+  for (int64_t piece = blockIdx.x; piece < last_border; piece += gridDim.x) {
+    const int64_t border = (piece + 1) * kPiece, begin = piece * kPiece;
+    const int row = a.sorted_row[border];
+    if (a.sorted_row[border - 1] != row) continue;
+    if (begin > 0 && a.sorted_row[begin - 1] == row) continue;  // begins earlier
+    // the run goes on while pieces begin with its row; 64 pieces are looked at at a time
+    int64_t next = piece + 2;
+    for (;; next += 64) {
+      const int64_t p = next + lane;
+      const uint64_t ended = __ballot(p > last_border || a.sorted_row[p * kPiece] != row);
+      if (ended != 0) {
+        next += __ffsll((unsigned long long)ended) - 1;
+        break;
+      }
     }
-    write_row<T>(a, row, c, n, acc);
+    const int64_t pieces = next - piece, share = ceil_div(pieces, 4);
+    const int64_t q0 = piece + wave * share, q1 = q0 + share < piece + pieces ? q0 + share : piece + pieces;
+    for (int64_t c0 = int64_t(blockIdx.y) * 64 * E; c0 < a.dim; c0 += int64_t(gridDim.y) * 64 * E) {
+      const int64_t c = c0 + lane * E;
+      const int n = tail<E>(a.dim - c);
+      float acc[E] = {};
+      for (int64_t q = q0; q < q1; q += kAhead) {
+        Raw<float, E> r[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int64_t p = q + j < q1 ? q + j : q1 - 1;
+          r[j] = load_vec<float, E>(a.partial + (2 * p + (p == piece ? 1 : 0)) * a.dim + c, n);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (q + j < q1) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) acc[k] += r[j].get(k);
+          }
+      }
+      __syncthreads();  // the last columns' quarters are read
+      if (wave > 0) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) quarter[wave - 1][k * 64 + lane] = acc[k];
+      }
+      __syncthreads();
+      if (wave == 0 && n > 0) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+#pragma unroll
+          for (int k = 0; k < E; ++k) acc[k] += quarter[w][k * 64 + lane];
+        write_row<T, E>(a, row, c, n, acc);
+      }
+    }
   }
 }
 
 template <typename T, typename I>
 void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
-  const int rows = int(sort_rows(a.vocab));
-  const int64_t ranges = (a.vocab + rows - 1) / rows;
-  hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(unsigned(ranges)), dim3(kSortThreads),
-                     kSortWaves * rows * sizeof(int), s, a, rows);
-  const int64_t pieces = (a.tokens + kPiece - 1) / kPiece;
-  if (pieces == 0) return;
-  int64_t cols = (a.dim + kThreads * 8 - 1) / (kThreads * 8);
-  if (cols > 1024) cols = 1024;
-  hipLaunchKernelGGL((embedding_sum_kernel<T>), dim3(unsigned(pieces), unsigned(cols)), dim3(kThreads), 0, s, a);
+  const int shift = sort_shift(a.vocab);
+  const int64_t ranges = int64_t(1) << shift, rows = ceil_div(a.vocab, ranges);
+  int bits = 0;
+  while ((1 << bits) < rows) ++bits;
+  const unsigned sorting = unsigned(a.vocab < ranges ? a.vocab : ranges);
+  const unsigned zeroing = a.accumulate ? 0 : grid_of(a.vocab * a.dim, kSortThreads * kVec<T>);
+  hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(sorting + zeroing), dim3(kSortThreads),
+                     kSortWaves * rows * sizeof(int), s, a, sorting, shift, int(rows), bits);
+  const int64_t pieces = ceil_div(a.tokens, kPiece), chunks = ceil_div(ceil_div(a.dim, kVec<T>), 64);
+  if (pieces > 0)
+    hipLaunchKernelGGL((embedding_sum_kernel<T>), dim3(grid_of(pieces * chunks, 4)), dim3(kThreads), 0, s, a);
   if (pieces > 1)
-    hipLaunchKernelGGL((embedding_join_kernel<T>), dim3(unsigned(pieces - 1), unsigned(cols)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((embedding_join_kernel<T>), dim3(grid_of(pieces - 1, 1), unsigned(chunks < 64 ? chunks : 64)),
+                       dim3(kThreads), 0, s, a);
 }
 
 // Two vectors a lane and up to four waves a row: 65536 rows of 4096 bf16 (20132 distinct of 131072) in
@@ -308,7 +433,7 @@ template <typename T, typename I>
 void lookup(int64_t tokens, const void* ids, int64_t vocab, int64_t dim, const void* table, float scale, void* out,
             hipStream_t s) {
   constexpr int NV = 2, NT = 4;
-  const int64_t vecs = (dim + kVec<T> - 1) / kVec<T>;
+  const int64_t vecs = ceil_div(dim, kVec<T>);
   const auto* i = static_cast<const I*>(ids);
   const auto* w = static_cast<const T*>(table);
   auto* o = static_cast<T*>(out);
@@ -316,13 +441,13 @@ void lookup(int64_t tokens, const void* ids, int64_t vocab, int64_t dim, const v
     int lshift = 0;
     while ((1 << lshift) < vecs) ++lshift;
     const int64_t per = int64_t(kThreads >> lshift) * NT;
-    hipLaunchKernelGGL((embedding_narrow_kernel<T, I, NT>), dim3(unsigned((tokens + per - 1) / per)), dim3(kThreads), 0,
+    hipLaunchKernelGGL((embedding_narrow_kernel<T, I, NT>), dim3(grid_of(tokens, per)), dim3(kThreads), 0,
                        s, tokens, i, vocab, int(dim), w, scale, o, lshift);
     return;
   }
   const int wshift = vecs <= 64 * NV ? 0 : vecs <= 128 * NV ? 1 : 2;
   const int64_t per = 4 >> wshift;
-  hipLaunchKernelGGL((embedding_rows_kernel<T, I, NV>), dim3(unsigned((tokens + per - 1) / per)), dim3(kThreads), 0, s,
+  hipLaunchKernelGGL((embedding_rows_kernel<T, I, NV>), dim3(grid_of(tokens, per)), dim3(kThreads), 0, s,
                      tokens, i, vocab, dim, w, scale, o, wshift);
 }
 

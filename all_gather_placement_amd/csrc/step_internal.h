@@ -100,14 +100,15 @@ int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, int param_dtype,
 int launch_embedding(int64_t tokens, const void* ids, int ids_dtype, int64_t vocab, int64_t dim, const void* table,
                      int dtype, float scale, void* out, void* stream);
 
-// The gradient's sort gives each workgroup a range of table rows; it finds the range's tokens by
-// reading all ids.  A range holds at most kSortMaxRows rows, and there are kSortRanges ranges (one
-// for each compute unit) where the table has that many rows.
+// The gradient's sort gives each of 2^shift workgroups the table rows v with v mod 2^shift its number;
+// it finds their tokens by reading all ids.  There is one for each compute unit at least, and none has
+// more than kSortMaxRows rows.
 constexpr int kSortMaxRows = 512;
-constexpr int kSortRanges = 256;
-inline int64_t sort_rows(int64_t vocab) {
-  const int64_t r = (vocab + kSortRanges - 1) / kSortRanges;
-  return r < 1 ? 1 : (r > kSortMaxRows ? kSortMaxRows : r);
+constexpr int kSortMinShift = 8;
+inline int sort_shift(int64_t vocab) {
+  int s = kSortMinShift;
+  while (vocab > int64_t(kSortMaxRows) << s) ++s;
+  return s;
 }
 // Sorted tokens are summed in pieces of kPiece.  A run of equal ids that crosses a border of pieces
 // leaves fp32 partial sums, at most two for each piece, that a second kernel adds in order.
