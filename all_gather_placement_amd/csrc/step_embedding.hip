@@ -244,6 +244,25 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   if (found == 0) return;
   __syncthreads();
 
+  // A wave's tokens of the range wait in a queue in LDS until there are 64 of them, so that the work on
+  // them does not grow with the tokens of other ranges.  Only this wave uses its queue and its places,
+  // and its LDS accesses stay in order.
+  __shared__ int2 queues[kSortWaves][128];  // token, row of the range
+  int2* queue = queues[wave];
+  int waiting = 0;
+  const auto place_tokens = [&](int n) {
+    const int2 q = lane < n ? queue[lane] : int2{0, 0};
+    const uint64_t active = n == 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+    const uint64_t same = same_row(q.y, active, bits, lane);
+    if (lane < n) {
+      const int first = __hip_atomic_load(mine + q.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      const int at = first + __popcll(same & ((uint64_t(1) << lane) - 1));
+      a.sorted_token[at] = q.x;
+      a.sorted_row[at] = int(unsigned(q.y) << shift | range);
+      if (lane == 63 - __clzll((long long)same))  // the last of its row: the next place
+        __hip_atomic_store(mine + q.y, at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+  };
   for (int64_t t0 = begin; t0 < end; t0 += 64 * kAhead) {
     I v[kAhead];
 #pragma unroll
@@ -254,19 +273,20 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
       const bool here = uint64_t(id) < vocab && (unsigned(id) & mask) == range;
       const uint64_t active = __ballot(here);
       if (active == 0) continue;
-      const int row = here ? int(unsigned(id) >> shift) : 0;
-      const uint64_t same = same_row(row, active, bits, lane);
-      if (here) {
-        // only this wave uses this place, and its LDS accesses stay in order
-        const int first = __hip_atomic_load(mine + row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        const int at = first + __popcll(same & ((uint64_t(1) << lane) - 1));
-        a.sorted_token[at] = int(t0 + j * 64 + lane);
-        a.sorted_row[at] = int(id);
-        if (lane == 63 - __clzll((long long)same))  // the last of its row: the next place
-          __hip_atomic_store(mine + row, at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-      }
+      if (here)
+        queue[waiting + __popcll(active & ((uint64_t(1) << lane) - 1))] =
+            int2{int(t0 + j * 64 + lane), int(unsigned(id) >> shift)};
+      waiting += __popcll(active);
+      if (waiting < 64) continue;
+      __builtin_amdgcn_wave_barrier();
+      place_tokens(64);
+      waiting -= 64;
+      if (lane < waiting) queue[lane] = queue[64 + lane];
+      __builtin_amdgcn_wave_barrier();
     }
   }
+  __builtin_amdgcn_wave_barrier();
+  place_tokens(waiting);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -287,11 +307,11 @@ __device__ __forceinline__ void write_row(const EmbeddingBwdArgs& a, int row, in
   store_vec<T, E>(out, n, f);
 }
 
-// A wave's item: 64 vectors of columns of a piece of kPiece sorted tokens.  Eight rows of dy are in
-// flight at a time; they are added in order.
+// A wave's item: 64 vectors of columns of a piece of kPiece sorted tokens.  Sixteen
+// rows of dy are in flight at a time; they are added in order.
 template <typename T>
 __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t piece, int64_t c, int total) {
-  constexpr int E = kVec<T>, kAhead = 8;
+  constexpr int E = kVec<T>, kAhead = 16;
   const int lane = threadIdx.x & 63;
   const int64_t begin = piece * kPiece;
   const int cnt = int(total - begin < kPiece ? total - begin : kPiece);
@@ -350,16 +370,17 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArg
 // vectors of columns, its waves a quarter of the run's pieces each, in order; the quarters meet in LDS.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdArgs a) {
-  constexpr int E = kVec<T>, kAhead = 8;
+  constexpr int E = kVec<T>, kAhead = 64 / E;
   __shared__ float quarter[3][64 * E];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int total = *a.num_sorted;
   const int64_t last_border = (int64_t(total) - 1) / kPiece;  // pieces 0 .. last_border hold tokens
   for (int64_t piece = blockIdx.x; piece < last_border; piece += gridDim.x) {
     const int64_t border = (piece + 1) * kPiece, begin = piece * kPiece;
-    const int row = a.sorted_row[border];
-    if (a.sorted_row[border - 1] != row) continue;
-    if (begin > 0 && a.sorted_row[begin - 1] == row) continue;  // begins earlier
+    // read together: a wait for each would cost more
+    const int row = a.sorted_row[border], inner = a.sorted_row[border - 1];
+    const int before = a.sorted_row[begin > 0 ? begin - 1 : 0];
+    if (inner != row || (begin > 0 && before == row)) continue;  // no run crosses here, or it begins earlier
     // the run goes on while pieces begin with its row; 64 pieces are looked at at a time
     int64_t next = piece + 2;
     for (;; next += 64) {
