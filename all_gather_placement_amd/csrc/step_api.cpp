@@ -82,9 +82,19 @@ inline void cut(int64_t numel, int dtype, uint32_t* chunks, uint32_t* last) {
   *last = uint32_t(numel - (n - 1) * c);
 }
 
-inline int norm_grid(uint32_t chunks) { return int(std::min<uint32_t>(chunks, kNormMaxWgs)); }
+inline int norm_grid(uint32_t chunks) { return int(std::min<uint32_t>(chunks, kNormWgs)); }
+inline int clip_grid(uint32_t chunks) { return int(std::min<uint32_t>(chunks, kNormMaxWgs)); }
 
-// Calls f(table) for every launch that the non-empty tensors need; stops at the first error.
+int64_t num_chunks(int32_t n, const int64_t* numels, int dtype) {
+  const int64_t c = norm_chunk_elems(dtype);
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) total += (numels[i] + c - 1) / c;
+  return total;
+}
+// Whether one workgroup does a whole call, in one launch.
+bool one_workgroup(int64_t chunks) { return chunks > 0 && chunks <= kNormOneWgChunks; }
+
+// Calls f(table) for every launch that the non-empty tensors need, stops at the first error.
 template <typename Table, int kBatch, typename Fill, typename F>
 int for_tables(int32_t n, const int64_t* numels, int dtype, Fill&& fill, F&& f) {
   Table t;
@@ -127,20 +137,24 @@ int64_t norm_workspace(int32_t n, const int64_t* numels, int dtype) {
 int enqueue_norm(int32_t n, const void* const* grads, const int64_t* numels, int dtype, double* sumsq, float* norm,
                  void* workspace, void* stream) {
   double* partial = static_cast<double*>(workspace) + 2;
+  const bool one = one_workgroup(num_chunks(n, numels, dtype));
   int used = 0;
   const int e = for_tables<NormTable, kNormBatch>(
       n, numels, dtype, [&](NormEntry& t, int32_t i) { t.p = grads[i]; },
-      [&](const NormTable& t) {
-        const int grid = norm_grid(t.chunks);
+      [&](NormTable& t) {
+        const int grid = one ? 1 : norm_grid(t.chunks);
+        t.sumsq = one ? sumsq : nullptr;
+        t.norm = one ? norm : nullptr;
         const int err = launch_norm_partial(t, dtype, partial + used, grid, stream);
         used += grid;
         return err;
       });
-  return e != 0 ? e : launch_norm_finish(partial, used, sumsq, norm, stream);
+  return e != 0 ? e : launch_norm_finish(partial, used, one ? nullptr : sumsq, one ? nullptr : norm, stream);
 }
 
+// Clipping by *sumsq, or, where `sum_to` is given, one workgroup's sum and clipping by it.
 int enqueue_clip(int32_t n, const void* const* grads, void* const* outs, const int64_t* numels, int dtype,
-                 const double* sumsq, double max_norm, float* norm, void* stream) {
+                 const double* sumsq, double* sum_to, double max_norm, float* norm, void* stream) {
   bool first = true;
   const int e = for_tables<ClipTable, kClipBatch>(
       n, numels, dtype,
@@ -148,8 +162,10 @@ int enqueue_clip(int32_t n, const void* const* grads, void* const* outs, const i
         t.p = grads[i];
         t.out = outs[i];
       },
-      [&](const ClipTable& t) {
-        const int err = launch_clip(t, dtype, sumsq, max_norm, first ? norm : nullptr, norm_grid(t.chunks), stream);
+      [&](ClipTable& t) {
+        t.sum_to = sum_to;
+        const int grid = sum_to != nullptr ? 1 : clip_grid(t.chunks);
+        const int err = launch_clip(t, dtype, sumsq, max_norm, first ? norm : nullptr, grid, stream);
         first = false;
         return err;
       });
@@ -157,6 +173,7 @@ int enqueue_clip(int32_t n, const void* const* grads, void* const* outs, const i
   ClipTable none;  // no elements: the norm alone
   none.count = 0;
   none.chunks = 0;
+  none.sum_to = nullptr;
   return launch_clip(none, dtype, sumsq, max_norm, norm, 1, stream);
 }
 
@@ -220,7 +237,7 @@ tide_status tide_grad_clip(int32_t num_tensors, const void* const* grads, void* 
   std::vector<Range> scalars{range_of(sumsq, 8)};
   if (norm != nullptr) scalars.push_back(range_of(norm, 4));
   if (clip_overlaps(num_tensors, grads, outs, numels, dtype, scalars)) return TIDE_ERR_INVALID;
-  return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, sumsq, max_norm, norm, stream));
+  return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, sumsq, nullptr, max_norm, norm, stream));
 } catch (const std::bad_alloc&) {
   return TIDE_ERR_NOMEM;
 }
@@ -239,8 +256,10 @@ tide_status tide_clip_grad_norm(int32_t num_tensors, const void* const* grads, v
   if (norm != nullptr) scalars.push_back(range_of(norm, 4));
   if (clip_overlaps(num_tensors, grads, outs, numels, dtype, scalars)) return TIDE_ERR_INVALID;
   double* s = sumsq != nullptr ? sumsq : static_cast<double*>(workspace);
+  if (one_workgroup(num_chunks(num_tensors, numels, dtype)))
+    return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, s, s, max_norm, norm, stream));
   int e = enqueue_norm(num_tensors, grads, numels, dtype, s, norm, workspace, stream);
-  if (e == 0) e = enqueue_clip(num_tensors, grads, outs, numels, dtype, s, max_norm, nullptr, stream);
+  if (e == 0) e = enqueue_clip(num_tensors, grads, outs, numels, dtype, s, nullptr, max_norm, nullptr, stream);
   return status_of(e);
 } catch (const std::bad_alloc&) {
   return TIDE_ERR_NOMEM;

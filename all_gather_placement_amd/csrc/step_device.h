@@ -35,6 +35,9 @@ __device__ __forceinline__ u32x2 load8(const void* p) {
   return *reinterpret_cast<const TIDE_STEP_GLOBAL u32x2_any*>((uintptr_t)p);
 }
 
+// Keeps the scheduler from putting the use of one load before the next load of a group.
+__device__ __forceinline__ void loads_first() { __builtin_amdgcn_sched_barrier(0); }
+
 __device__ __forceinline__ float widen(bf16_t b) { return __uint_as_float(static_cast<unsigned int>(b) << 16); }
 __device__ __forceinline__ float widen(float f) { return f; }
 

@@ -13,11 +13,15 @@ namespace tide_step {
 
 // A tensor is cut into chunks of 16 KiB, four 16-byte vectors for each of 256 threads; the last
 // chunk of a tensor holds what is left.  A launch walks the chunks of up to kNormBatch tensors in
-// order, workgroup b taking b, b + grid, ...  Tensors are named in the kernel's arguments (4 KiB),
-// so a call needs no device table, copy or event.
+// order.  Tensors are named in the kernel's arguments (4 KiB), so a call needs no device table, copy
+// or event.
 constexpr int kNormThreads = 256;
 constexpr int kNormChunkBytes = 16384;
-constexpr int kNormMaxWgs = 2048;
+constexpr int kNormWgs = 1024;           // of a sum: workgroup b takes chunks b, b + grid, ... (196 us; 2048: 212)
+constexpr int kNormMaxWgs = 1 << 20;     // of clipping: a workgroup lives for one chunk
+// A call of up to so many chunks is one workgroup's, in one launch: as fast on the GPU (8 chunks: sum 3.7 us,
+// clipping 7.1, in two and three launches 4.3 and 6.7; 16 chunks 5.3 and 11.4 against 4.4 and 6.7).
+constexpr int kNormOneWgChunks = 8;
 constexpr int64_t kMaxNormElems = int64_t(1) << 42;
 constexpr int norm_chunk_elems(int dtype) { return kNormChunkBytes / (dtype == TIDE_BF16 ? 2 : 4); }
 
@@ -30,6 +34,8 @@ constexpr int kNormBatch = 250;
 struct NormTable {
   int32_t count;
   uint32_t chunks;
+  double* sumsq;  // not NULL (one of the two): the launch is one workgroup and its sum is the result
+  float* norm;
   NormEntry e[kNormBatch];
 };
 static_assert(sizeof(NormTable) <= 4032, "kernel arguments stay within 4 KiB");
@@ -44,13 +50,14 @@ constexpr int kClipBatch = 160;
 struct ClipTable {
   int32_t count;
   uint32_t chunks;
+  double* sum_to;  // not NULL: the launch is one workgroup, which first writes the sum of squares there
   ClipEntry e[kClipBatch];
 };
 static_assert(sizeof(ClipTable) <= 4032, "kernel arguments stay within 4 KiB");
 
 // Each returns a hipError_t.
 int launch_norm_partial(const NormTable& t, int dtype, double* partial, int grid, void* stream);
-int launch_norm_finish(const double* partial, int n, double* sumsq, float* norm, void* stream);
+int launch_norm_finish(const double* partial, int n, double* sumsq, float* norm, void* stream);  // nothing to write: no launch
 int launch_clip(const ClipTable& t, int dtype, const double* sumsq, double max_norm, float* norm, int grid,
                 void* stream);
 

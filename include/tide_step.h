@@ -56,8 +56,7 @@ enum {
  *   sumsq        device, one double, 8-byte aligned, or NULL
  *   norm         device, one float, 4-byte aligned, or NULL
  * Result: sumsq = sum of squares of every element, norm = sqrt(sumsq) rounded to fp32; 0 for no
- * elements.  Squares and sums are held in 64 bits (squares of eight neighbours may be added in 32
- * bits first, where none of them leaves its range), so no finite gradient overflows; a NaN or an
+ * elements.  Squares and sums are held in 64 bits, so no finite gradient overflows; a NaN or an
  * infinity anywhere gives NaN or infinity.  A data-parallel job adds up `sumsq` over its ranks and
  * passes the total to tide_grad_clip.
  * Errors: TIDE_ERR_INVALID (null or misaligned pointer, negative count, unknown dtype, total above
