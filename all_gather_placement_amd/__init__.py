@@ -15,6 +15,7 @@ from .step import (  # noqa: F401
     grad_norm,
     layer_norm,
     layer_norm_bwd,
+    load_step_binding,
     load_step_library,
     step_library_path,
 )

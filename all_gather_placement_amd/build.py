@@ -1,4 +1,5 @@
-"""Build libtide.so (C ABI + gfx950 kernels), libtide_step.so and libtide_probe.so in-tree with hipcc.
+"""Build libtide.so (C ABI + gfx950 kernels), libtide_step.so with its Python module _step.so, and
+libtide_probe.so in-tree with hipcc.
 
     python -m all_gather_placement_amd.build
 
@@ -17,9 +18,11 @@ from __future__ import annotations
 import ctypes
 import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,6 +34,8 @@ PROBE_LIB = os.path.join(PKG, "libtide_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 STEP_LIB = os.path.join(PKG, "libtide_step.so")
 STEP_SOURCES = ["step_api.cpp", "step_norm.hip", "step_layer_norm.hip", "step_embedding.hip"]
+STEP_BINDING = os.path.join(PKG, "_step.so")
+STEP_BINDING_SOURCES = ["step_binding.cpp"]
 ARCH = "gfx950"
 
 # Everything each library is compiled from (its sources and every header they include).
@@ -41,6 +46,8 @@ HASHED = {
                + [os.path.join(INCLUDE, "tide_probe.h")],
     STEP_LIB: [os.path.join(CSRC, f) for f in (*STEP_SOURCES, "step_internal.h", "step_device.h")]
               + [os.path.join(INCLUDE, f) for f in ("tide_step.h", "tide.h")],
+    STEP_BINDING: [os.path.join(CSRC, f) for f in STEP_BINDING_SOURCES]
+                  + [os.path.join(INCLUDE, f) for f in ("tide_step.h", "tide.h")],
 }
 ID_SYMBOL = {LIB: "tide_build_id", PROBE_LIB: "tide_probe_build_id", STEP_LIB: "tide_step_build_id"}
 
@@ -72,11 +79,34 @@ def source_hash(lib: str = LIB, extra=()) -> str:
     return h.hexdigest()[:16]
 
 
+BINDING_MARK = rb"tide_step_binding build id ([0-9a-f]{16})\0"
+
+
+def torch_flags() -> list:
+    """Compile flags of the Python module: torch's headers and the interpreter's."""
+    from torch.utils.cpp_extension import include_paths
+
+    dirs = [*include_paths(), sysconfig.get_paths()["include"]]
+    return ["-fvisibility=hidden", *(f for d in dirs for f in ("-isystem", d))]
+
+
+def torch_link_flags() -> list:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["-L" + PKG, "-l:" + os.path.basename(STEP_LIB), "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def built_id(lib: str = LIB):
     """Build id embedded in the library file at `lib`, or None if it is missing or carries none.
-    Loads the library (no HIP call is made by loading or by the id query)."""
+    Loads the library (no HIP call is made by loading or by the id query); the Python module's, which
+    would load torch, is found in the file."""
     if not os.path.exists(lib):
         return None
+    if lib == STEP_BINDING:
+        with open(lib, "rb") as fh:
+            found = re.search(BINDING_MARK, fh.read())
+        return found.group(1).decode() if found else None
     try:
         fn = getattr(ctypes.CDLL(lib), ID_SYMBOL[lib])
     except (OSError, AttributeError):
@@ -109,6 +139,7 @@ def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, prob
     if probe and out == LIB:
         build(verbose=verbose, extra=extra, out=PROBE_LIB, sources=PROBE_SOURCES, probe=False)
         build(verbose=verbose, extra=extra, out=STEP_LIB, sources=STEP_SOURCES, probe=False)
+        build(verbose=verbose, extra=extra, out=STEP_BINDING, sources=STEP_BINDING_SOURCES, probe=False)
     objdir = os.path.join(PKG, "_build", os.path.splitext(os.path.basename(out))[0])
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
@@ -120,7 +151,8 @@ def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, prob
     for src in sources:
         obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [cc, *compile_flags(extra), *id_flag, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+        more = torch_flags() if out == STEP_BINDING else []
+        cmd = [cc, *compile_flags(extra), *id_flag, *lang, *more, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         running.append(subprocess.Popen(cmd))
@@ -135,6 +167,8 @@ def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, prob
             "-Wl,-rpath,/opt/rocm/lib", "-L/opt/rocm/lib", "-lamdhip64"]
     if out == PROBE_LIB:
         link.append("-lhsa-runtime64")  # the DMA engines' rectangular copy (tide_probe_dma_rect_copies)
+    if out == STEP_BINDING:
+        link += torch_link_flags()
     if verbose:
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
@@ -156,7 +190,7 @@ def is_current(lib: str) -> bool:
 def ensure_built(verbose: bool = False) -> str:
     """Build the libraries if they are missing or were built from other sources (tests, smoke and
     benchmark entry points); returns the path of libtide.so."""
-    if not (is_current(LIB) and is_current(PROBE_LIB) and is_current(STEP_LIB)):
+    if not all(map(is_current, (LIB, PROBE_LIB, STEP_LIB, STEP_BINDING))):
         build(verbose=verbose)
     return LIB
 
