@@ -189,11 +189,20 @@ bool clip_overlaps(int32_t n, const void* const* grads, void* const* outs, const
   const int size = size_of(dtype);
   for (int32_t i = 0; i < n; ++i)
     if (numels[i] > 0) o.push_back({range_of(outs[i], numels[i] * size), i});
-  std::sort(o.begin(), o.end(), [](const Tagged& a, const Tagged& b) { return a.r.lo < b.r.lo; });
+  const auto lower = [](const Tagged& a, const Tagged& b) { return a.r.lo < b.r.lo; };
+  if (!std::is_sorted(o.begin(), o.end(), lower)) std::sort(o.begin(), o.end(), lower);
   for (size_t i = 1; i < o.size(); ++i)
     if (o[i].r.lo < o[i - 1].r.hi) return true;
+  auto near = o.begin();  // where the last range was found: lists are mostly in order of address
   const auto hits = [&](const Range& in, int32_t own) {
-    auto it = std::upper_bound(o.begin(), o.end(), in.lo, [](uintptr_t v, const Tagged& t) { return v < t.r.hi; });
+    const auto first = [&](auto it) {  // whether `it` is the first output that ends after in.lo
+      return (it == o.end() || in.lo < it->r.hi) && (it == o.begin() || std::prev(it)->r.hi <= in.lo);
+    };
+    if (near != o.end() && first(std::next(near)))
+      ++near;
+    else if (!first(near))
+      near = std::upper_bound(o.begin(), o.end(), in.lo, [](uintptr_t v, const Tagged& t) { return v < t.r.hi; });
+    auto it = near;
     for (; it != o.end() && it->r.lo < in.hi; ++it)
       if (it->tensor != own || it->r.lo != in.lo) return true;
     return false;

@@ -36,10 +36,11 @@ template <typename... Parts>
   PyErr_SetString(kind, s.str().c_str());
   throw Refused();
 }
-template <typename... Parts>
-inline void need(bool ok, const Parts&... parts) {
-  if (!ok) refuse(PyExc_ValueError, parts...);
-}
+// The message's parts are made only where they are needed: some cost more than the rest of a check.
+#define NEED(ok, ...)                                                      \
+  do {                                                                     \
+    if (__builtin_expect(!(ok), 0)) refuse(PyExc_ValueError, __VA_ARGS__); \
+  } while (0)
 
 void check(tide_status status, const char* where) {
   if (status == TIDE_OK) return;
@@ -105,18 +106,18 @@ struct Device {
   }
 };
 void on_gpu(const at::Tensor& t, const char* name) {
-  need(t.is_cuda(), name, " must be on the current device, got ", t.device().str());
+  NEED(t.is_cuda(), name, " must be on the current device, got ", t.device().str());
 }
 void on(const Device& d, const at::Tensor& t, const char* name) {
-  need(t.is_cuda() && t.get_device() == d.index, name, " must be on the current device (cuda:", d.index, "), got ",
+  NEED(t.is_cuda() && t.get_device() == d.index, name, " must be on the current device (cuda:", d.index, "), got ",
        t.device().str());
 }
 void like(const Device& d, const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape) {
   on(d, t, name);
-  need(t.scalar_type() == type, name, " must be of ", c10::toString(type), ", got ", c10::toString(t.scalar_type()));
-  need(t.sizes() == shape, name, " must have shape ", shape, ", got ", t.sizes());
+  NEED(t.scalar_type() == type, name, " must be of ", c10::toString(type), ", got ", c10::toString(t.scalar_type()));
+  NEED(t.sizes() == shape, name, " must have shape ", shape, ", got ", t.sizes());
 }
-void dense(const at::Tensor& t, const char* name) { need(t.is_contiguous(), name, " must be contiguous"); }
+void dense(const at::Tensor& t, const char* name) { NEED(t.is_contiguous(), name, " must be contiguous"); }
 inline void* at_of(Opt t) { return t == nullptr ? nullptr : t->data_ptr(); }
 
 // The caller's workspace if it is large enough, else a new one, kept alive until the call is enqueued.
@@ -128,9 +129,9 @@ struct Workspace {
     if (needed < 0) check(TIDE_ERR_INVALID, where);
     if (given != nullptr) {
       on(d, *given, "workspace");
-      need(given->scalar_type() == at::kByte, "workspace must be of torch.uint8");
+      NEED(given->scalar_type() == at::kByte, "workspace must be of torch.uint8");
       dense(*given, "workspace");
-      need(given->numel() >= needed, "workspace must hold ", needed, " bytes, got ", given->numel());
+      NEED(given->numel() >= needed, "workspace must hold ", needed, " bytes, got ", given->numel());
     } else {
       own = d.empty({needed}, at::kByte);
       given = &own;
@@ -192,16 +193,16 @@ struct List {
       ~Drop() { Py_DECREF(o); }
     } drop{seq};
     const Py_ssize_t size = PySequence_Fast_GET_SIZE(seq);
-    need(size <= INT32_MAX, "too many ", name);
+    NEED(size <= INT32_MAX, "too many ", name);
     p.reserve(size_t(size));
     n.reserve(size_t(size));
     for (Py_ssize_t i = 0; i < size; ++i) {
       const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(seq, i), name);
       on(d, t, name);
       if (i == 0) type = t.scalar_type();
-      need(is_float(t.scalar_type()), name, " must be of ", kFloats, ", got ", c10::toString(t.scalar_type()));
-      need(t.scalar_type() == type, "all ", name, " must have one dtype");
-      need(t.is_contiguous(), "all ", name, " must be contiguous");
+      NEED(is_float(t.scalar_type()), name, " must be of ", kFloats, ", got ", c10::toString(t.scalar_type()));
+      NEED(t.scalar_type() == type, "all ", name, " must have one dtype");
+      NEED(t.is_contiguous(), "all ", name, " must be contiguous");
       p.push_back(t.data_ptr());
       n.push_back(t.numel());
     }
@@ -212,15 +213,15 @@ struct List {
 List outputs(const Device& d, PyObject* o, PyObject* grads, const List& g) {
   if (o == Py_None) return g;
   List outs(d, o, "outs");
-  need(outs.n == g.n, "outs must have the gradients' sizes");
-  need(g.p.empty() || outs.type == g.type, "outs must have the gradients' dtype");
+  NEED(outs.n == g.n, "outs must have the gradients' sizes");
+  NEED(g.p.empty() || outs.type == g.type, "outs must have the gradients' dtype");
   return outs;
 }
 void one_value(const Device& d, Opt t, const char* name, at::ScalarType type) {
   if (t == nullptr) return;
   on(d, *t, name);
-  need(t->scalar_type() == type, name, " must be of ", c10::toString(type), ", got ", c10::toString(t->scalar_type()));
-  need(t->numel() == 1, name, " must hold one value");
+  NEED(t->scalar_type() == type, name, " must be of ", c10::toString(type), ", got ", c10::toString(t->scalar_type()));
+  NEED(t->numel() == 1, name, " must hold one value");
 }
 // The first of a list tells a tensor of the host apart before the device is asked for.
 void first_on_gpu(PyObject* list, const char* name) {
@@ -228,7 +229,7 @@ void first_on_gpu(PyObject* list, const char* name) {
     if (PyObject* o = PySequence_GetItem(list, 0)) {
       const bool host = THPVariable_Check(o) && !THPVariable_Unpack(o).is_cuda();
       Py_DECREF(o);
-      need(!host, name, " must be on the current device");
+      NEED(!host, name, " must be on the current device");
     }
   if (PyErr_Occurred()) throw Refused();
 }
@@ -304,20 +305,20 @@ PyObject* clip_grad_norm(Args a, Py_ssize_t n) {
 struct Matrix {
   int64_t rows, cols, stride;
   Matrix(const at::Tensor& t, const char* name) {
-    need(t.dim() >= 1, name, " must have at least one dimension");
+    NEED(t.dim() >= 1, name, " must have at least one dimension");
     cols = t.size(-1);
-    need(cols >= 1, name, " must have a last dimension of at least one");
+    NEED(cols >= 1, name, " must have a last dimension of at least one");
     rows = t.numel() / cols;
     stride = cols;
     if (t.is_contiguous()) return;
-    need(t.dim() == 2 && (t.stride(1) == 1 || cols == 1) && t.stride(0) >= cols, name,
+    NEED(t.dim() == 2 && (t.stride(1) == 1 || cols == 1) && t.stride(0) >= cols, name,
          " must be contiguous, or a matrix whose rows are");
     stride = t.stride(0);
   }
 };
 void float_on(const Device& d, const at::Tensor& t, const char* name) {
   on(d, t, name);
-  need(is_float(t.scalar_type()), name, " must be of ", kFloats, ", got ", c10::toString(t.scalar_type()));
+  NEED(is_float(t.scalar_type()), name, " must be of ", kFloats, ", got ", c10::toString(t.scalar_type()));
 }
 // The parameters' one dtype: that of the first given, x's if there is none.
 struct Params {
@@ -327,9 +328,9 @@ struct Params {
   void add(const Device& d, Opt t, const char* name, int64_t cols) {
     if (t == nullptr) return;
     float_on(d, *t, name);
-    need(t->dim() == 1 && t->size(0) == cols, name, " must have shape [", cols, "], got ", t->sizes());
+    NEED(t->dim() == 1 && t->size(0) == cols, name, " must have shape [", cols, "], got ", t->sizes());
     dense(*t, name);
-    need(!any || t->scalar_type() == type, "weight, bias and their gradients must have one dtype");
+    NEED(!any || t->scalar_type() == type, "weight, bias and their gradients must have one dtype");
     type = t->scalar_type();
     any = true;
   }
@@ -404,7 +405,7 @@ PyObject* layer_norm_bwd(Args a, Py_ssize_t n) {
 
 void ids_on(const Device& d, const at::Tensor& ids) {
   on(d, ids, "ids");
-  need(is_id(ids.scalar_type()), "ids must be of torch.int32 or torch.int64, got ", c10::toString(ids.scalar_type()));
+  NEED(is_id(ids.scalar_type()), "ids must be of torch.int32 or torch.int64, got ", c10::toString(ids.scalar_type()));
   dense(ids, "ids");
 }
 
@@ -417,7 +418,7 @@ PyObject* embedding(Args a, Py_ssize_t n) {
   ids_on(d, ids);
   float_on(d, table, "table");
   dense(table, "table");
-  need(table.dim() == 2 && table.size(1) >= 1, "table must be [vocab, dim] with dim at least one");
+  NEED(table.dim() == 2 && table.size(1) >= 1, "table must be [vocab, dim] with dim at least one");
   c10::SmallVector<int64_t, 6> shape(ids.sizes().begin(), ids.sizes().end());
   shape.push_back(table.size(1));
   const Output out(a[3], "out", [&] { return d.empty(shape, table.scalar_type()); });
@@ -438,14 +439,14 @@ PyObject* embedding_bwd(Args a, Py_ssize_t n) {
   ids_on(d, ids);
   float_on(d, dy, "dy");
   dense(dy, "dy");
-  need(dy.dim() == ids.dim() + 1 && dy.sizes().slice(0, size_t(ids.dim())) == ids.sizes(),
+  NEED(dy.dim() == ids.dim() + 1 && dy.sizes().slice(0, size_t(ids.dim())) == ids.sizes(),
        "dy must have shape ids.shape + (dim,)");
   const int64_t vocab = whole(a[2]), dim = dy.size(-1);
-  need(dim >= 1, "dy must have a last dimension of at least one");
-  need(vocab >= 0, "vocab must not be negative");
+  NEED(dim >= 1, "dy must have a last dimension of at least one");
+  NEED(vocab >= 0, "vocab must not be negative");
   const int accumulate = PyObject_IsTrue(a[5]);
   if (accumulate < 0) throw Refused();
-  need(a[4] != Py_None || accumulate == 0, "accumulate needs the gradient to add to as `out`");
+  NEED(a[4] != Py_None || accumulate == 0, "accumulate needs the gradient to add to as `out`");
   const Output out(a[4], "out", [&] { return d.empty({vocab, dim}, dy.scalar_type()); });
   like(d, *out.t, "out", dy.scalar_type(), {vocab, dim});
   dense(*out.t, "out");
