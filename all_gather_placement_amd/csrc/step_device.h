@@ -3,7 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include <cstring>
+#include <type_traits>
 
 namespace tide_step {
 
@@ -77,39 +77,102 @@ struct Raw {
   }
 };
 
-// The first n (of E) elements at p, zeros beyond; n <= 0 reads nothing.
-template <typename T, int E, bool kOnce = false>
-__device__ __forceinline__ Raw<T, E> load_vec(const T* p, int n) {
+template <typename T, int E, bool kOnce>
+__device__ __forceinline__ Raw<T, E> load_whole(const T* p) {
   Raw<T, E> r;
-  if (n >= E) {
-    if constexpr (r.kWords == 2) {
-      const u32x2 v = load8(p);
-      r.w[0] = v[0];
-      r.w[1] = v[1];
-    } else {
+  if constexpr (r.kWords == 2) {
+    const u32x2 v = load8(p);
+    r.w[0] = v[0];
+    r.w[1] = v[1];
+  } else {
 #pragma unroll
-      for (int q = 0; q < r.kWords / 4; ++q) {
-        const u32x4 v = load16<kOnce>(reinterpret_cast<const char*>(p) + 16 * q);
+    for (int q = 0; q < r.kWords / 4; ++q) {
+      const u32x4 v = load16<kOnce>(reinterpret_cast<const char*>(p) + 16 * q);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) r.w[4 * q + k] = v[k];
+      for (int k = 0; k < 4; ++k) r.w[4 * q + k] = v[k];
+    }
+  }
+  return r;
+}
+// Moves elements s, s + 1, ... (s < E) to the front, zeros behind them.
+template <typename T, int E>
+__device__ __forceinline__ void drop_front(Raw<T, E>& r, int s) {
+  constexpr int W = Raw<T, E>::kWords;
+  const int words = sizeof(T) == 2 ? s >> 1 : s;
+#pragma unroll
+  for (int bit = W / 2; bit >= 1; bit >>= 1)
+    if (words & bit) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) r.w[k] = k + bit < W ? r.w[k + bit] : 0;
+    }
+  if (sizeof(T) == 2 && (s & 1)) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) r.w[k] = r.w[k] >> 16 | (k + 1 < W ? r.w[k + 1] << 16 : 0);
+  }
+}
+// The first n (of E) elements at p, zeros beyond; n <= 0 reads nothing.  With kWhole rows are of whole
+// vectors and n is E or more where it is not 0 or less.  Otherwise, where the row has E elements
+// (`wide`), its end is read as the vector that ends there: a load for each element, and their waits,
+// would take longer than all the rest of a row.
+template <typename T, int E, bool kOnce, bool kWhole>
+__device__ __forceinline__ Raw<T, E> load_vec(const T* p, int n, bool wide) {
+  Raw<T, E> r;
+#pragma unroll
+  for (int q = 0; q < r.kWords; ++q) r.w[q] = 0;
+  if constexpr (kWhole) {
+    if (n > 0) r = load_whole<T, E, kOnce>(p);
+  } else if (wide) {
+    if (n > 0) r = load_whole<T, E, kOnce>(n < E ? p + (n - E) : p);
+    if (n > 0 && n < E) drop_front(r, E - n);
+  } else {
+    unsigned int e[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      e[i] = 0;
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          e[i] = p[i];
+        else
+          e[i] = __float_as_uint(p[i]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < r.kWords; ++q) {
+      if constexpr (sizeof(T) == 2)
+        r.w[q] = e[2 * q] | e[2 * q + 1] << 16;
+      else
+        r.w[q] = e[q];
+    }
+  }
+  return r;
+}
+// N vectors, vector j at p[j] + c, as load_vec: their loads follow each other without a branch or a
+// wait.  The addresses p are made before, where all lanes are active: a lane that is not has no value
+// to give.
+template <typename T, int E, int N, bool kOnce, bool kWhole>
+__device__ __forceinline__ void load_vecs(Raw<T, E> (&r)[N], const T* const (&p)[N], int64_t c, int n, bool wide) {
+  if (kWhole || wide) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int q = 0; q < Raw<T, E>::kWords; ++q) r[j].w[q] = 0;
+    if (n > 0) {
+      const int64_t at = !kWhole && n < E ? c + (n - E) : c;
+#pragma unroll
+      for (int j = 0; j < N; ++j) r[j] = load_whole<T, E, kOnce>(p[j] + at);
+      loads_first();
+      if (!kWhole && n < E) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) drop_front(r[j], E - n);
       }
     }
   } else {
 #pragma unroll
-    for (int q = 0; q < r.kWords; ++q) r.w[q] = 0;
-#pragma unroll
-    for (int i = 0; i < E - 1; ++i)
-      if (i < n) {
-        if constexpr (sizeof(T) == 2)
-          r.w[i >> 1] |= static_cast<unsigned int>(p[i]) << (16 * (i & 1));
-        else
-          r.w[i] = __float_as_uint(p[i]);
-      }
+    for (int j = 0; j < N; ++j) r[j] = load_vec<T, E, kOnce, false>(p[j] + c, n, false);
   }
-  return r;
 }
-// The first n (of E) values of f to p, rounded.
-template <typename T, int E, bool kOnce = false>
+// The first n (of E) values of f to p, rounded; kWhole as for load_vec.
+template <typename T, int E, bool kOnce, bool kWhole>
 __device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[E]) {
   if (n >= E) {
     unsigned int w[Raw<T, E>::kWords];
@@ -124,11 +187,17 @@ __device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[E]) {
 #pragma unroll
     for (int q = 0; q < Raw<T, E>::kWords / 4; ++q)
       store16<kOnce>(reinterpret_cast<char*>(p) + 16 * q, u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]});
-  } else {
+  } else if constexpr (!kWhole) {
 #pragma unroll
     for (int i = 0; i < E - 1; ++i)
       if (i < n) p[i] = narrow<T>(f[i]);
   }
+}
+// f(whole) as a constant: rows of `cols` elements are of whole vectors of E, or not.
+template <int E, typename F>
+void with_whole(int64_t cols, F&& f) {
+  if (cols % E == 0) f(std::true_type());
+  else f(std::false_type());
 }
 // Elements of a 16-byte vector.
 template <typename T>

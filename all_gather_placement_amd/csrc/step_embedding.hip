@@ -33,12 +33,12 @@ inline unsigned grid_of(int64_t n, int64_t per) {
 // Lookup
 // ---------------------------------------------------------------------------------------------
 
-template <typename T, int E>
+template <typename T, int E, bool kWhole>
 __device__ __forceinline__ void store_scaled(T* out, int n, const Raw<T, E>& r, bool inside, float scale) {
   float f[E];
 #pragma unroll
   for (int k = 0; k < E; ++k) f[k] = inside ? r.get(k) * scale : 0.0f;
-  store_vec<T, E, true>(out, n, f);
+  store_vec<T, E, true, kWhole>(out, n, f);
 }
 template <int E>
 __device__ __forceinline__ int tail(int64_t n) {
@@ -47,7 +47,7 @@ __device__ __forceinline__ int tail(int64_t n) {
 
 // Rows of 64 vectors and more: a row goes to 1 << wshift waves of a workgroup of four, a lane holding
 // NV vectors at a time.
-template <typename T, typename I, int NV>
+template <typename T, typename I, int NV, bool kWhole>
 __global__ __launch_bounds__(kThreads) void embedding_rows_kernel(int64_t tokens, const I* __restrict__ ids,
                                                                   int64_t vocab, int64_t dim,
                                                                   const T* __restrict__ table, float scale,
@@ -66,19 +66,19 @@ __global__ __launch_bounds__(kThreads) void embedding_rows_kernel(int64_t tokens
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int64_t c = c0 + (v * 64 + lane) * E;
-        r[v] = load_vec<T, E>(row + c, inside ? tail<E>(dim - c) : 0);
+        r[v] = load_vec<T, E, false, kWhole>(row + c, inside ? tail<E>(dim - c) : 0, true);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int64_t c = c0 + (v * 64 + lane) * E;
-        if (c < dim) store_scaled<T, E>(o + c, tail<E>(dim - c), r[v], inside, scale);
+        if (c < dim) store_scaled<T, E, kWhole>(o + c, tail<E>(dim - c), r[v], inside, scale);
       }
     }
   }
 }
 
 // Narrow rows: a group of 1 << lshift lanes for each of NT tokens in turn.
-template <typename T, typename I, int NT>
+template <typename T, typename I, int NT, bool kWhole>
 __global__ __launch_bounds__(kThreads) void embedding_narrow_kernel(int64_t tokens, const I* __restrict__ ids,
                                                                     int64_t vocab, int dim,
                                                                     const T* __restrict__ table, float scale,
@@ -94,13 +94,13 @@ __global__ __launch_bounds__(kThreads) void embedding_narrow_kernel(int64_t toke
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const bool inside = id[i] >= 0 && id[i] < vocab;
-      r[i] = load_vec<T, E>(table + (inside ? id[i] * dim : 0) + c, inside ? dim - c : 0);
+      r[i] = load_vec<T, E, false, kWhole>(table + (inside ? id[i] * dim : 0) + c, inside ? dim - c : 0, dim >= E);
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int64_t t = t0 + i * groups;
       if (t < tokens && c < dim)
-        store_scaled<T, E>(out + t * dim + c, dim - c, r[i], id[i] >= 0 && id[i] < vocab, scale);
+        store_scaled<T, E, kWhole>(out + t * dim + c, dim - c, r[i], id[i] >= 0 && id[i] < vocab, scale);
     }
   }
 }
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
     const int64_t end = a.vocab * a.dim;
     for (int64_t e = (int64_t(blockIdx.x - ranges) * kSortThreads + threadIdx.x) * N; e < end;
          e += int64_t(gridDim.x - ranges) * kSortThreads * N)
-      store_vec<T, N>(static_cast<T*>(a.dtable) + e, tail<N>(end - e), none);
+      store_vec<T, N, false, false>(static_cast<T*>(a.dtable) + e, tail<N>(end - e), none);
     return;
   }
   extern __shared__ int count[];  // [kSortWaves][most_rows]: tokens of a wave's part, then their places
@@ -293,23 +293,23 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
 // Gradient: sums
 // ---------------------------------------------------------------------------------------------
 
-template <typename T, int E>
+template <typename T, int E, bool kWhole>
 __device__ __forceinline__ void write_row(const EmbeddingBwdArgs& a, int row, int64_t c, int n, const float (&acc)[E]) {
   T* out = static_cast<T*>(a.dtable) + int64_t(row) * a.dim + c;
   float f[E];
 #pragma unroll
   for (int k = 0; k < E; ++k) f[k] = acc[k] * a.scale;
   if (a.accumulate) {
-    const Raw<T, E> old = load_vec<T, E>(out, n);
+    const Raw<T, E> old = load_vec<T, E, false, kWhole>(out, n, a.dim >= E);
 #pragma unroll
     for (int k = 0; k < E; ++k) f[k] += old.get(k);
   }
-  store_vec<T, E>(out, n, f);
+  store_vec<T, E, false, kWhole>(out, n, f);
 }
 
 // A wave's item: 64 vectors of columns of a piece of kPiece sorted tokens.  Sixteen
 // rows of dy are in flight at a time; they are added in order.
-template <typename T>
+template <typename T, bool kWhole>
 __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t piece, int64_t c, int total) {
   constexpr int E = kVec<T>, kAhead = 16;
   const int lane = threadIdx.x & 63;
@@ -326,12 +326,14 @@ __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t pie
   int row = __builtin_amdgcn_readlane(rows, 0);
   bool open = row == __builtin_amdgcn_readlane(rows, kPiece + 1);  // the run began in an earlier piece
   for (int i0 = 0; i0 < cnt; i0 += kAhead) {
-    Raw<T, E> r[kAhead];
+    const T* from[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {  // beyond the end the last token again, so that no branch parts the loads
+    for (int j = 0; j < kAhead; ++j) {  // beyond the end the last token again
       const int64_t t = __builtin_amdgcn_readlane(tokens, i0 + j < cnt ? i0 + j : cnt - 1);
-      r[j] = load_vec<T, E, true>(static_cast<const T*>(a.dy) + t * a.dim + c, n);
+      from[j] = static_cast<const T*>(a.dy) + t * a.dim;
     }
+    Raw<T, E> r[kAhead];
+    load_vecs<T, E, kAhead, true, kWhole>(r, from, c, n, a.dim >= E);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j;
@@ -342,9 +344,9 @@ __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t pie
       if (next == row && i + 1 < cnt) continue;
       if (n > 0) {
         if (open || next == row)
-          store_vec<float, E>(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
+          store_vec<float, E, false, kWhole>(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
         else
-          write_row<T, E>(a, row, c, n, acc);
+          write_row<T, E, kWhole>(a, row, c, n, acc);
       }
 #pragma unroll
       for (int k = 0; k < E; ++k) acc[k] = 0.0f;
@@ -354,7 +356,7 @@ __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t pie
   }
 }
 
-template <typename T>
+template <typename T, bool kWhole>
 __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArgs a) {
   constexpr int E = kVec<T>;
   const int total = *a.num_sorted;
@@ -362,13 +364,13 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   for (int64_t item = int64_t(blockIdx.x) * 4 + wave; item < items; item += int64_t(gridDim.x) * 4) {
     const int64_t piece = item / chunks;
-    sum_piece<T>(a, piece, ((item - piece * chunks) * 64 + lane) * E, total);
+    sum_piece<T, kWhole>(a, piece, ((item - piece * chunks) * 64 + lane) * E, total);
   }
 }
 
 // Adds the partial sums of a run that begins in a piece and ends in a later one: a workgroup takes 64
 // vectors of columns, its waves a quarter of the run's pieces each, in order; the quarters meet in LDS.
-template <typename T>
+template <typename T, bool kWhole>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdArgs a) {
   constexpr int E = kVec<T>, kAhead = 64 / E;
   __shared__ float quarter[3][64 * E];
@@ -398,12 +400,14 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdAr
       const int n = tail<E>(a.dim - c);
       float acc[E] = {};
       for (int64_t q = q0; q < q1; q += kAhead) {
-        Raw<float, E> r[kAhead];
+        const float* from[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const int64_t p = q + j < q1 ? q + j : q1 - 1;
-          r[j] = load_vec<float, E>(a.partial + (2 * p + (p == piece ? 1 : 0)) * a.dim + c, n);
+          from[j] = a.partial + (2 * p + (p == piece ? 1 : 0)) * a.dim;
         }
+        Raw<float, E> r[kAhead];
+        load_vecs<float, E, kAhead, false, kWhole>(r, from, c, n, a.dim >= E);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
           if (q + j < q1) {
@@ -422,14 +426,95 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdAr
         for (int w = 0; w < 3; ++w)
 #pragma unroll
           for (int k = 0; k < E; ++k) acc[k] += quarter[w][k * 64 + lane];
-        write_row<T, E>(a, row, c, n, acc);
+        write_row<T, E, kWhole>(a, row, c, n, acc);
       }
     }
   }
 }
 
-template <typename T, typename I>
+// Few tokens: a workgroup for each, which looks at all ids, goes on if its own is the first of its row,
+// and sums the row's tokens in ascending order.
+template <typename T, typename I, bool kWhole>
+__global__ __launch_bounds__(kThreads) void embedding_direct_kernel(EmbeddingBwdArgs a) {
+  constexpr int E = kVec<T>, kAhead = 16, kMasks = kDirectTokens / 64;
+  __shared__ uint64_t masks[kMasks];
+  __shared__ int list[kDirectTokens];
+  const I* __restrict__ ids = static_cast<const I*>(a.ids);
+  const int tokens = int(a.tokens), lane = threadIdx.x & 63;
+  const int64_t row = ids[blockIdx.x];
+  if (uint64_t(row) >= uint64_t(a.vocab)) return;
+  I id[kDirectTokens / kThreads];
+#pragma unroll
+  for (int j = 0; j < kDirectTokens / kThreads; ++j) {
+    const int t = j * kThreads + threadIdx.x;
+    id[j] = t < tokens ? ids[t] : I(-1);
+  }
+#pragma unroll
+  for (int j = 0; j < kDirectTokens / kThreads; ++j) {
+    const uint64_t same = __ballot(int64_t(id[j]) == row);
+    if (lane == 0) masks[(j * kThreads + threadIdx.x) / 64] = same;
+  }
+  __syncthreads();
+  int before[kMasks + 1] = {};
+#pragma unroll
+  for (int k = 0; k < kMasks; ++k) before[k + 1] = before[k] + __popcll(masks[k]);
+  // this workgroup's token is the row's first one?
+  const int first = blockIdx.x / 64;
+#pragma unroll
+  for (int k = 0; k < kMasks; ++k) {
+    const uint64_t earlier = k < first ? ~uint64_t(0) : k == first ? (uint64_t(1) << (blockIdx.x & 63)) - 1 : 0;
+    if ((masks[k] & earlier) != 0) return;
+  }
+#pragma unroll
+  for (int j = 0; j < kDirectTokens / kThreads; ++j) {
+    const int t = j * kThreads + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kMasks; ++k)
+      if (t / 64 == k && ((masks[k] >> lane) & 1)) list[before[k] + __popcll(masks[k] & ((uint64_t(1) << lane) - 1))] = t;
+  }
+  __syncthreads();
+  const int n = before[kMasks];
+  // a wave takes 64 vectors of columns; all of its lanes go along, those beyond the last column too
+  for (int64_t c0 = int64_t(threadIdx.x / 64) * 64 * E; c0 < a.dim; c0 += kThreads * E) {
+    const int64_t c = c0 + lane * E;
+    const int m = tail<E>(a.dim - c);
+    float acc[E] = {};
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      const int token = list[i0 + lane < n ? i0 + lane : n - 1];
+      const T* from[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        from[j] = static_cast<const T*>(a.dy) + int64_t(__builtin_amdgcn_readlane(token, j)) * a.dim;
+      Raw<T, E> r[kAhead];
+      load_vecs<T, E, kAhead, true, kWhole>(r, from, c, m, a.dim >= E);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j < n) {
+#pragma unroll
+          for (int k = 0; k < E; ++k) acc[k] += r[j].get(k);
+        }
+    }
+    if (m > 0) write_row<T, E, kWhole>(a, int(row), c, m, acc);
+  }
+}
+template <typename T>
+__global__ __launch_bounds__(kThreads) void embedding_zero_kernel(T* table, int64_t n) {
+  constexpr int E = kVec<T>;
+  const float none[E] = {};
+  for (int64_t e = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * E; e < n; e += int64_t(gridDim.x) * kThreads * E)
+    store_vec<T, E, false, false>(table + e, tail<E>(n - e), none);
+}
+
+template <typename T, typename I, bool kWhole>
 void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
+  if (a.tokens <= kDirectTokens) {
+    if (!a.accumulate)
+      hipLaunchKernelGGL((embedding_zero_kernel<T>), dim3(grid_of(a.vocab * a.dim, kThreads * kVec<T>)), dim3(kThreads),
+                         0, s, static_cast<T*>(a.dtable), a.vocab * a.dim);
+    if (a.tokens > 0)
+      hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
+    return;
+  }
   const int shift = sort_shift(a.vocab);
   const int64_t ranges = int64_t(1) << shift, rows = ceil_div(a.vocab, ranges);
   int bits = 0;
@@ -439,11 +524,13 @@ void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(sorting + zeroing), dim3(kSortThreads),
                      kSortWaves * rows * sizeof(int), s, a, sorting, shift, int(rows), bits);
   const int64_t pieces = ceil_div(a.tokens, kPiece), chunks = ceil_div(ceil_div(a.dim, kVec<T>), 64);
-  if (pieces > 0)
-    hipLaunchKernelGGL((embedding_sum_kernel<T>), dim3(grid_of(pieces * chunks, 4)), dim3(kThreads), 0, s, a);
-  if (pieces > 1)
-    hipLaunchKernelGGL((embedding_join_kernel<T>), dim3(grid_of(pieces - 1, 1), unsigned(chunks < 64 ? chunks : 64)),
-                       dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((embedding_sum_kernel<T, kWhole>), dim3(grid_of(pieces * chunks, 4)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((embedding_join_kernel<T, kWhole>), dim3(grid_of(pieces - 1, 1), unsigned(chunks < 64 ? chunks : 64)),
+                     dim3(kThreads), 0, s, a);
+}
+template <typename T, typename I>
+void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
+  with_whole<kVec<T>>(a.dim, [&](auto w) { gradient<T, I, decltype(w)::value>(a, s); });
 }
 
 // Two vectors a lane and up to four waves a row: 65536 rows of 4096 bf16 (20132 distinct of 131072) in
@@ -458,18 +545,20 @@ void lookup(int64_t tokens, const void* ids, int64_t vocab, int64_t dim, const v
   const auto* i = static_cast<const I*>(ids);
   const auto* w = static_cast<const T*>(table);
   auto* o = static_cast<T*>(out);
-  if (vecs < 64) {
-    int lshift = 0;
-    while ((1 << lshift) < vecs) ++lshift;
-    const int64_t per = int64_t(kThreads >> lshift) * NT;
-    hipLaunchKernelGGL((embedding_narrow_kernel<T, I, NT>), dim3(grid_of(tokens, per)), dim3(kThreads), 0,
-                       s, tokens, i, vocab, int(dim), w, scale, o, lshift);
-    return;
-  }
-  const int wshift = vecs <= 64 * NV ? 0 : vecs <= 128 * NV ? 1 : 2;
-  const int64_t per = 4 >> wshift;
-  hipLaunchKernelGGL((embedding_rows_kernel<T, I, NV>), dim3(grid_of(tokens, per)), dim3(kThreads), 0, s,
-                     tokens, i, vocab, dim, w, scale, o, wshift);
+  with_whole<kVec<T>>(dim, [&](auto wh) {
+    constexpr bool whole = decltype(wh)::value;
+    if (vecs < 64) {
+      int lshift = 0;
+      while ((1 << lshift) < vecs) ++lshift;
+      const int64_t per = int64_t(kThreads >> lshift) * NT;
+      hipLaunchKernelGGL((embedding_narrow_kernel<T, I, NT, whole>), dim3(grid_of(tokens, per)), dim3(kThreads), 0, s,
+                         tokens, i, vocab, int(dim), w, scale, o, lshift);
+      return;
+    }
+    const int wshift = vecs <= 64 * NV ? 0 : vecs <= 128 * NV ? 1 : 2;
+    hipLaunchKernelGGL((embedding_rows_kernel<T, I, NV, whole>), dim3(grid_of(tokens, 4 >> wshift)), dim3(kThreads), 0,
+                       s, tokens, i, vocab, dim, w, scale, o, wshift);
+  });
 }
 
 }  // namespace

@@ -60,13 +60,14 @@ __device__ __forceinline__ float block_sum(float v, float (&lds)[kMaxWaves]) {
 // Forward
 // ---------------------------------------------------------------------------------------------
 
-template <typename T, typename PT>
+template <typename T, typename PT, bool kWhole>
 struct Affine {
   static constexpr int E = kVec<T>;
   Raw<PT, E> w, b;
   __device__ __forceinline__ void load(const LayerNormArgs& a, int c, int n) {
-    if (a.weight != nullptr) w = load_vec<PT, E>(static_cast<const PT*>(a.weight) + c, n);
-    if (a.bias != nullptr) b = load_vec<PT, E>(static_cast<const PT*>(a.bias) + c, n);
+    const bool wide = a.cols >= E;
+    if (a.weight != nullptr) w = load_vec<PT, E, false, kWhole>(static_cast<const PT*>(a.weight) + c, n, wide);
+    if (a.bias != nullptr) b = load_vec<PT, E, false, kWhole>(static_cast<const PT*>(a.bias) + c, n, wide);
   }
   template <bool kOnce>
   __device__ __forceinline__ void store(const LayerNormArgs& a, T* y, int n, const Raw<T, E>& r, float mean,
@@ -77,23 +78,23 @@ struct Affine {
       const float xhat = (r.get(k) - mean) * rstd;
       o[k] = (a.weight != nullptr ? xhat * w.get(k) : xhat) + (a.bias != nullptr ? b.get(k) : 0.0f);
     }
-    store_vec<T, E, kOnce>(y, n, o);
+    store_vec<T, E, kOnce, kWhole>(y, n, o);
   }
 };
 
 // Narrow rows: a group of L lanes for each, one vector a lane.
 constexpr int kNarrowThreads = 256;
 
-template <typename T, typename PT, int L, bool kOnce>
+template <typename T, typename PT, int L, bool kOnce, bool kWhole>
 __global__ __launch_bounds__(kNarrowThreads) void layer_norm_narrow_kernel(LayerNormArgs a) {
   constexpr int E = kVec<T>, kGroups = kNarrowThreads / L;
   const int D = int(a.cols), c = (threadIdx.x % L) * E, n = D - c;
   const float inv = 1.0f / float(D);
-  Affine<T, PT> affine;
+  Affine<T, PT, kWhole> affine;
   affine.load(a, c, n);
   for (int64_t row = int64_t(blockIdx.x) * kGroups + threadIdx.x / L; row < a.rows;
        row += int64_t(gridDim.x) * kGroups) {
-    const Raw<T, E> r = load_vec<T, E, kOnce>(static_cast<const T*>(a.x) + row * a.x_stride + c, n);
+    const Raw<T, E> r = load_vec<T, E, kOnce, kWhole>(static_cast<const T*>(a.x) + row * a.x_stride + c, n, D >= E);
     float sum = 0;
 #pragma unroll
     for (int k = 0; k < E; ++k) sum += r.get(k);
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(kNarrowThreads) void layer_norm_narrow_kernel(Layer
 
 // Rows of up to kMaxWaves * 64 * NV vectors: a workgroup holds RB rows at a time in registers, NV
 // vectors of each in a lane, and joins the waves' sums of all of them at one barrier.
-template <typename T, typename PT, int NV, int RB, bool kOnce>
+template <typename T, typename PT, int NV, int RB, bool kOnce, bool kWhole>
 __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_rows_kernel(LayerNormArgs a) {
   constexpr int E = kVec<T>;
   __shared__ float lds[2][RB * kMaxWaves];
@@ -129,10 +130,10 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_rows_kernel(LayerNo
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E;
-        r[i][v] = load_vec<T, E, kOnce>(x + c, row0 + i < a.rows ? D - c : 0);
+        r[i][v] = load_vec<T, E, kOnce, kWhole>(x + c, row0 + i < a.rows ? D - c : 0, true);
       }
     }
-    Affine<T, PT> affine[NV];
+    Affine<T, PT, kWhole> affine[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E;
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_wide_kernel(LayerNorm
     T* y = static_cast<T*>(a.y) + row * a.y_stride;
     float sum = 0;
     for (int64_t c = int64_t(threadIdx.x) * E; c < D; c += kWideThreads * E) {
-      const Raw<T, E> r = load_vec<T, E>(x + c, tail<E>(D - c));
+      const Raw<T, E> r = load_vec<T, E, false, false>(x + c, tail<E>(D - c), true);
 #pragma unroll
       for (int k = 0; k < E; ++k) sum += r.get(k);
     }
@@ -208,7 +209,7 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_wide_kernel(LayerNorm
     float sq = 0;
     for (int64_t c = int64_t(threadIdx.x) * E; c < D; c += kWideThreads * E) {
       const int n = tail<E>(D - c);
-      const Raw<T, E> r = load_vec<T, E>(x + c, n);
+      const Raw<T, E> r = load_vec<T, E, false, false>(x + c, n, true);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         const float d = r.get(k) - mean;
@@ -223,17 +224,17 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_wide_kernel(LayerNorm
     }
     for (int64_t c = int64_t(threadIdx.x) * E; c < D; c += kWideThreads * E) {
       const int n = tail<E>(D - c);
-      const Raw<T, E> r = load_vec<T, E>(x + c, n);
+      const Raw<T, E> r = load_vec<T, E, false, false>(x + c, n, true);
       Raw<PT, E> rw, rb;
-      if (w != nullptr) rw = load_vec<PT, E>(w + c, n);
-      if (b != nullptr) rb = load_vec<PT, E>(b + c, n);
+      if (w != nullptr) rw = load_vec<PT, E, false, false>(w + c, n, true);
+      if (b != nullptr) rb = load_vec<PT, E, false, false>(b + c, n, true);
       float o[E];
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         const float xhat = (r.get(k) - mean) * rstd;
         o[k] = (w != nullptr ? xhat * rw.get(k) : xhat) + (b != nullptr ? rb.get(k) : 0.0f);
       }
-      store_vec<T, E>(y + c, n, o);
+      store_vec<T, E, false, false>(y + c, n, o);
     }
   }
 }
@@ -243,19 +244,19 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_wide_kernel(LayerNorm
 // ---------------------------------------------------------------------------------------------
 
 // Narrow rows: as the forward kernel; the groups' sums over their rows meet in LDS, in order.
-template <typename T, typename PT, int L, bool kOnce>
+template <typename T, typename PT, int L, bool kOnce, bool kWhole>
 __global__ __launch_bounds__(kNarrowThreads) void layer_norm_bwd_narrow_kernel(LayerNormBwdArgs a) {
   constexpr int E = kVec<T>, kGroups = kNarrowThreads / L;
   __shared__ float join[kNarrowThreads * E];
   const int D = int(a.cols), c = (threadIdx.x % L) * E, n = D - c;
   const float inv = 1.0f / float(D);
   Raw<PT, E> rw;
-  if (a.weight != nullptr) rw = load_vec<PT, E>(static_cast<const PT*>(a.weight) + c, n);
+  if (a.weight != nullptr) rw = load_vec<PT, E, false, kWhole>(static_cast<const PT*>(a.weight) + c, n, D >= E);
   float dw[E] = {}, db[E] = {};
   for (int64_t row = int64_t(blockIdx.x) * kGroups + threadIdx.x / L; row < a.rows;
        row += int64_t(gridDim.x) * kGroups) {
-    const Raw<T, E> rx = load_vec<T, E, kOnce>(static_cast<const T*>(a.x) + row * a.x_stride + c, n);
-    const Raw<T, E> rd = load_vec<T, E, kOnce>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, n);
+    const Raw<T, E> rx = load_vec<T, E, kOnce, kWhole>(static_cast<const T*>(a.x) + row * a.x_stride + c, n, D >= E);
+    const Raw<T, E> rd = load_vec<T, E, kOnce, kWhole>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, n, D >= E);
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s1 = 0, s2 = 0;
 #pragma unroll
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(kNarrowThreads) void layer_norm_bwd_narrow_kernel(L
       const float g = a.weight != nullptr ? rd.get(k) * rw.get(k) : rd.get(k);
       o[k] = rstd * (g - s1 - xhat * s2);
     }
-    store_vec<T, E, kOnce>(static_cast<T*>(a.dx) + row * a.dx_stride + c, n, o);
+    store_vec<T, E, kOnce, kWhole>(static_cast<T*>(a.dx) + row * a.dx_stride + c, n, o);
   }
   if (a.partial == nullptr) return;
   float* part = a.partial + int64_t(blockIdx.x) * 2 * padded(D);
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(kNarrowThreads) void layer_norm_bwd_narrow_kernel(L
 
 // Rows of up to kMaxWaves * 64 * NV vectors: RB rows at a time, as the forward kernel; the sums down
 // the columns stay in registers from the workgroup's first row to its last.
-template <typename T, typename PT, int NV, int RB, bool kOnce>
+template <typename T, typename PT, int NV, int RB, bool kOnce, bool kWhole>
 __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_rows_kernel(LayerNormBwdArgs a) {
   constexpr int E = kVec<T>;
   __shared__ float lds[2][2 * RB * kMaxWaves];
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_rows_kernel(Lay
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E;
-    if (a.weight != nullptr) rw[v] = load_vec<PT, E>(static_cast<const PT*>(a.weight) + c, D - c);
+    if (a.weight != nullptr) rw[v] = load_vec<PT, E, false, kWhole>(static_cast<const PT*>(a.weight) + c, D - c, true);
 #pragma unroll
     for (int k = 0; k < E; ++k) dw[v][k] = db[v][k] = 0.0f;
   }
@@ -329,8 +330,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_rows_kernel(Lay
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E;
-        rx[i][v] = load_vec<T, E, kOnce>(x + c, in ? D - c : 0);
-        rd[i][v] = load_vec<T, E, kOnce>(dy + c, in ? D - c : 0);
+        rx[i][v] = load_vec<T, E, kOnce, kWhole>(x + c, in ? D - c : 0, true);
+        rd[i][v] = load_vec<T, E, kOnce, kWhole>(dy + c, in ? D - c : 0, true);
       }
     }
     float s[2 * RB];
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_rows_kernel(Lay
           const float g = a.weight != nullptr ? d * rw[v].get(k) : d;
           o[k] = rstd[i] * (g - m1 - xhat * m2);
         }
-        store_vec<T, E, kOnce>(dx + c, n, o);
+        store_vec<T, E, kOnce, kWhole>(dx + c, n, o);
       }
     }
   }
@@ -383,8 +384,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_rows_kernel(Lay
   for (int v = 0; v < NV; ++v) {
     const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E, n = D - c;
     if (n <= 0) continue;
-    store_vec<float, E>(part + c, n, dw[v]);
-    store_vec<float, E>(part + padded(D) + c, n, db[v]);
+    store_vec<float, E, false, kWhole>(part + c, n, dw[v]);
+    store_vec<float, E, false, kWhole>(part + padded(D) + c, n, db[v]);
   }
 }
 
@@ -405,9 +406,9 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_wide_kernel(Layer
     float s1 = 0, s2 = 0;
     for (int64_t c = int64_t(threadIdx.x) * E; c < D; c += kWideThreads * E) {
       const int n = tail<E>(D - c);
-      const Raw<T, E> rx = load_vec<T, E>(x + c, n), rd = load_vec<T, E>(dy + c, n);
+      const Raw<T, E> rx = load_vec<T, E, false, false>(x + c, n, true), rd = load_vec<T, E, false, false>(dy + c, n, true);
       Raw<PT, E> rw;
-      if (w != nullptr) rw = load_vec<PT, E>(w + c, n);
+      if (w != nullptr) rw = load_vec<PT, E, false, false>(w + c, n, true);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         const float xhat = k < n ? (rx.get(k) - mean) * rstd : 0.0f;
@@ -420,9 +421,9 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_wide_kernel(Layer
     s2 = block_sum(s2, lds[parity][1]) * inv;
     for (int64_t c = int64_t(threadIdx.x) * E; c < D; c += kWideThreads * E) {
       const int n = tail<E>(D - c);
-      const Raw<T, E> rx = load_vec<T, E>(x + c, n), rd = load_vec<T, E>(dy + c, n);
+      const Raw<T, E> rx = load_vec<T, E, false, false>(x + c, n, true), rd = load_vec<T, E, false, false>(dy + c, n, true);
       Raw<PT, E> rw;
-      if (w != nullptr) rw = load_vec<PT, E>(w + c, n);
+      if (w != nullptr) rw = load_vec<PT, E, false, false>(w + c, n, true);
       float o[E];
 #pragma unroll
       for (int k = 0; k < E; ++k) {
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_wide_kernel(Layer
         const float g = w != nullptr ? rd.get(k) * rw.get(k) : rd.get(k);
         o[k] = rstd * (g - s1 - xhat * s2);
       }
-      store_vec<T, E>(dx + c, n, o);
+      store_vec<T, E, false, false>(dx + c, n, o);
     }
   }
 }
@@ -444,8 +445,8 @@ __global__ __launch_bounds__(64) void layer_norm_bwd_cols_kernel(LayerNormBwdArg
   const int n = tail<E>(D - c);
   float dw[E] = {}, db[E] = {};
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    const Raw<T, E> rx = load_vec<T, E>(static_cast<const T*>(a.x) + row * a.x_stride + c, n);
-    const Raw<T, E> rd = load_vec<T, E>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, n);
+    const Raw<T, E> rx = load_vec<T, E, false, false>(static_cast<const T*>(a.x) + row * a.x_stride + c, n, true);
+    const Raw<T, E> rd = load_vec<T, E, false, false>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, n, true);
     const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < E; ++k) {
@@ -454,8 +455,8 @@ __global__ __launch_bounds__(64) void layer_norm_bwd_cols_kernel(LayerNormBwdArg
     }
   }
   float* part = a.partial + int64_t(blockIdx.y) * 2 * padded(D);
-  store_vec<float, E>(part + c, n, dw);
-  store_vec<float, E>(part + padded(D) + c, n, db);
+  store_vec<float, E, false, false>(part + c, n, dw);
+  store_vec<float, E, false, false>(part + padded(D) + c, n, db);
 }
 
 // Adds the workgroups' partial sums: a workgroup takes 64 columns, a thread four of them and every
@@ -539,22 +540,24 @@ bool with_bwd_rows(int64_t vecs, F&& f) {
 // 8192 x 8192 bf16 backward 72 us instead of 81, 32760 x 5120 forward 119 instead of 124; tensors that
 // fit lose up to 10% that way (8192 x 4096 forward: 26 instead of 24).
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
-template <typename F>
-void with_once(int64_t bytes, F&& f) {
-  if (bytes > kCacheBytes) f(Int<1>());
-  else f(Int<0>());
+template <int E, typename F>
+void with_form(int64_t bytes, int64_t cols, F&& f) {
+  with_whole<E>(cols, [&](auto whole) {
+    if (bytes > kCacheBytes) f(std::true_type(), whole);
+    else f(std::false_type(), whole);
+  });
 }
 
 template <typename T, typename PT>
 void forward(const LayerNormArgs& a, hipStream_t s) {
   const int64_t vecs = ceil_div(a.cols, kVec<T>);
-  with_once(2 * a.rows * a.cols * int64_t(sizeof(T)), [&](auto o) {
-    constexpr bool once = decltype(o)::value != 0;
+  with_form<kVec<T>>(2 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {
+    constexpr bool once = decltype(o)::value, whole = decltype(w)::value;
     if (vecs <= 64) {
       with_lanes(vecs, [&](auto l) {
         constexpr int L = decltype(l)::value;
         const int64_t grid = min64(ceil_div(a.rows, kNarrowThreads / L), kMaxGrid);
-        hipLaunchKernelGGL((layer_norm_narrow_kernel<T, PT, L, once>), dim3(unsigned(grid)), dim3(kNarrowThreads), 0, s,
+        hipLaunchKernelGGL((layer_norm_narrow_kernel<T, PT, L, once, whole>), dim3(unsigned(grid)), dim3(kNarrowThreads), 0, s,
                            a);
       });
       return;
@@ -562,7 +565,7 @@ void forward(const LayerNormArgs& a, hipStream_t s) {
     const bool fits = with_rows(vecs, a.rows, [&](auto nv, auto rb, int waves) {
       constexpr int NV = decltype(nv)::value, RB = decltype(rb)::value;
       const int64_t grid = min64(ceil_div(a.rows, RB), kMaxGrid);
-      hipLaunchKernelGGL((layer_norm_rows_kernel<T, PT, NV, RB, once>), dim3(unsigned(grid)), dim3(waves * 64), 0, s, a);
+      hipLaunchKernelGGL((layer_norm_rows_kernel<T, PT, NV, RB, once, whole>), dim3(unsigned(grid)), dim3(waves * 64), 0, s, a);
     });
     if (!fits)
       hipLaunchKernelGGL((layer_norm_wide_kernel<T, PT>), dim3(unsigned(min64(a.rows, kMaxGrid))), dim3(kWideThreads),
@@ -576,17 +579,17 @@ void backward(LayerNormBwdArgs a, int groups, hipStream_t s) {
   const int64_t vecs = ceil_div(a.cols, kVec<T>);
   if (!params) a.partial = nullptr;
   if (a.rows > 0)
-    with_once(3 * a.rows * a.cols * int64_t(sizeof(T)), [&](auto o) {
-      constexpr bool once = decltype(o)::value != 0;
+    with_form<kVec<T>>(3 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {
+      constexpr bool once = decltype(o)::value, whole = decltype(w)::value;
       if (vecs <= 64) {
         with_lanes(vecs, [&](auto l) {
-          hipLaunchKernelGGL((layer_norm_bwd_narrow_kernel<T, PT, decltype(l)::value, once>), dim3(unsigned(groups)),
+          hipLaunchKernelGGL((layer_norm_bwd_narrow_kernel<T, PT, decltype(l)::value, once, whole>), dim3(unsigned(groups)),
                              dim3(kNarrowThreads), 0, s, a);
         });
         return;
       }
       const bool fits = with_bwd_rows(vecs, [&](auto nv, auto rb, int waves) {
-        hipLaunchKernelGGL((layer_norm_bwd_rows_kernel<T, PT, decltype(nv)::value, decltype(rb)::value, once>),
+        hipLaunchKernelGGL((layer_norm_bwd_rows_kernel<T, PT, decltype(nv)::value, decltype(rb)::value, once, whole>),
                            dim3(unsigned(groups)), dim3(waves * 64), 0, s, a);
       });
       if (fits) return;
