@@ -376,7 +376,7 @@ bool embedding_ok(int64_t tokens, const void* ids, int ids_dtype, int64_t vocab,
 bool rows_ok(const void* p, int64_t rows, int dtype) { return rows == 0 || (p != nullptr && aligned(p, size_of(dtype))); }
 
 struct EmbeddingPlan {
-  int64_t token, row, count, partial, bytes;  // offsets in the workspace
+  int64_t token, row, count, last, runs, partial, bytes;  // offsets in the workspace
 };
 EmbeddingPlan embedding_plan(int64_t tokens, int64_t dim) {
   const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
@@ -384,8 +384,10 @@ EmbeddingPlan embedding_plan(int64_t tokens, int64_t dim) {
   p.count = 0;
   p.token = 16;
   p.row = p.token + up(tokens * 4);
-  p.partial = p.row + up(tokens * 4);
   const int64_t pieces = (tokens + kPiece - 1) / kPiece;
+  p.last = p.row + up(tokens * 4);
+  p.runs = p.last + up(pieces * 4);
+  p.partial = p.runs + up(pieces * int64_t(sizeof(EmbeddingRun)));
   p.bytes = p.partial + up(pieces * 2 * dim * 4);
   return p;
 }
@@ -440,6 +442,8 @@ tide_status tide_embedding_bwd(int64_t tokens, const void* ids, int32_t ids_dtyp
                            reinterpret_cast<int32_t*>(ws + p.token),
                            reinterpret_cast<int32_t*>(ws + p.row),
                            reinterpret_cast<int32_t*>(ws + p.count),
+                           reinterpret_cast<int32_t*>(ws + p.last),
+                           reinterpret_cast<EmbeddingRun*>(ws + p.runs),
                            reinterpret_cast<float*>(ws + p.partial)};
   return status_of(launch_embedding_bwd(a, dtype, ids_dtype, stream));
 }

@@ -111,15 +111,9 @@ __global__ __launch_bounds__(kThreads) void embedding_narrow_kernel(int64_t toke
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-
-// Id k of a 16-byte vector.
-template <typename I>
-__device__ __forceinline__ int64_t id_of(u32x4 v, int k) {
-  if constexpr (sizeof(I) == 4)
-    return int(v[k]);
-  else
-    return int64_t(uint64_t(v[2 * k]) | uint64_t(v[2 * k + 1]) << 32);
-}
+constexpr int kRowBits = 9;   // of a row's number within its range
+constexpr int kListed = 448;  // tokens of a wave's list (with the counts less than 64 KiB of LDS)
+static_assert((1 << kRowBits) == kSortMaxRows, "a list's entry is a token of the wave's part and a row");
 
 // Inclusive sum over the wave.
 __device__ __forceinline__ int wave_scan(int v) {
@@ -148,6 +142,11 @@ __device__ __forceinline__ int block_exclusive(int v, int* lds, int* total) {
   return before + incl - v;
 }
 
+// Lanes of m below this one.
+__device__ __forceinline__ int lanes_before(uint64_t m) {
+  return int(__builtin_amdgcn_mbcnt_hi(unsigned(m >> 32), __builtin_amdgcn_mbcnt_lo(unsigned(m), 0)));
+}
+
 // The lanes whose `row` equals this lane's, of those in `active`.  A range seldom has more than two
 // different rows among 64 tokens: the first few are taken one by one, what is left by the rows' bits.
 __device__ __forceinline__ uint64_t same_row(int row, uint64_t active, int bits, int lane) {
@@ -169,11 +168,13 @@ __device__ __forceinline__ uint64_t same_row(int row, uint64_t active, int bits,
   return same;
 }
 
-// Workgroups below `ranges` sort; the others write zeros to the table, one 16-byte store a thread:
-// short-lived workgroups in order of address write fastest (131072 x 4096 bf16 with 1024 threads 169 us,
-// a wave for each row 194).  Rows that have tokens are written again by the sums, which costs less than
-// waiting for the sort and asking for each row whether it has any (237 us with the sums, 30 more than
-// they take one after the other).
+// Workgroups below `ranges` sort; the others, if any, write zeros to the table, one 16-byte store a
+// thread: short-lived workgroups in order of address write fastest (131072 x 4096 bf16 with 256 threads
+// 157 us, 1024 threads 169, a wave for each row 194).  Rows that have tokens are written again by the
+// sums, which costs less than asking for each row whether it has any (237 us with the sums, 30 more).
+//
+// 50021 tokens over 20011 rows: 21 us, of which reading the ids from the L2 is a third; with one list for
+// all of a range's tokens found twice 24, without lists 31, with contiguous ranges of rows 44.
 template <typename T, typename I>
 __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingBwdArgs a, unsigned ranges, int shift,
                                                                       int most_rows, int bits) {
@@ -188,42 +189,55 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   }
   extern __shared__ int count[];  // [kSortWaves][most_rows]: tokens of a wave's part, then their places
   __shared__ int lds[kSortWaves];
-  constexpr int E = kVec<I>;
-  const I* __restrict__ ids = static_cast<const I*>(a.ids);
+  __shared__ alignas(16) unsigned lists[kSortWaves][kListed];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const unsigned vocab = unsigned(a.vocab), range = blockIdx.x, mask = (1u << shift) - 1;
   const int rows = int((vocab - range + mask) >> shift);  // range, range + 2^shift, ...: at least one
   for (int i = threadIdx.x; i < kSortWaves * most_rows; i += kSortThreads) count[i] = 0;
-  __syncthreads();
 
   // each wave reads a part of the tokens of its own, in order
-  constexpr int kAhead = 8;  // loads in flight
-  const int64_t part = ceil_div(ceil_div(a.tokens, kSortWaves), 64 * E) * (64 * E);
-  const int64_t begin = wave * part, end = begin + part < a.tokens ? begin + part : a.tokens;
-  int* mine = count + wave * most_rows;
-  int below = 0;
-  const auto see = [&](int64_t id) {
-    const bool inside = uint64_t(id) < vocab;
-    const unsigned r = unsigned(id) & mask;
-    below += inside && r < range;
-    if (inside && r == range) atomicAdd(mine + (unsigned(id) >> shift), 1);
+  constexpr int kAhead = 16;  // loads in flight
+  const int64_t part = ceil_div(ceil_div(a.tokens, kSortWaves), 64) * 64;
+  const int64_t first_token = __builtin_amdgcn_readfirstlane(wave) * part;
+  const int end = int(first_token + part < a.tokens ? part : a.tokens > first_token ? a.tokens - first_token : 0);
+  const I* __restrict__ from = static_cast<const I*>(a.ids) + first_token;
+  const auto for_ids = [&](auto&& f) {  // f(token of the part, id), all lanes together; id -1 beyond the end
+    for (int t0 = 0; t0 < end; t0 += 64 * kAhead) {
+      I v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) v[j] = lane + j * 64 < end - t0 ? from[t0 + (lane + j * 64)] : I(-1);
+      loads_first();
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) f(t0 + j * 64 + lane, v[j]);
+    }
   };
-  int64_t t = begin;
-  for (; t + 64 * E * kAhead <= end; t += 64 * E * kAhead) {
-    u32x4 v[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) v[j] = load16(ids + t + (j * 64 + lane) * E);
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-      for (int k = 0; k < E; ++k) see(id_of<I>(v[j], k));
-  }
-  for (; t < end; t += 64 * kAhead) {
-    I v[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) v[j] = t + j * 64 + lane < end ? ids[t + j * 64 + lane] : I(-1);
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) see(v[j]);
+  const auto range_of = [&](I id) {  // ~0: outside the table
+    const bool inside = sizeof(I) == 4 || unsigned(uint64_t(id) >> 32) == 0;
+    return inside && unsigned(id) < vocab ? unsigned(id) & mask : ~0u;
+  };
+  // A wave lists its tokens of the range, so that most ranges read the ids once; those of a range that
+  // holds more than the list are found again.  Only this wave uses its list and its row of `count`, and
+  // its LDS accesses stay in order.
+  unsigned* list = lists[wave];
+  int* mine = count + wave * most_rows;
+  int below = 0, listed = 0;
+  for_ids([&](int t, I id) {
+    const unsigned r = range_of(id);
+    below += r < range;
+    const uint64_t here = __ballot(r == range);
+    if (here == 0) return;
+    const int at = listed + lanes_before(here);
+    if (r == range && at < kListed) list[at] = unsigned(t) << kRowBits | unsigned(id) >> shift;
+    listed += __popcll(here);
+  });
+  const bool all_listed = listed <= kListed && part <= (int64_t(1) << (32 - kRowBits));
+  __syncthreads();  // `count` is zero
+  if (all_listed) {
+    for (int i = lane; i < listed; i += 64) atomicAdd(mine + (list[i] & ((1 << kRowBits) - 1)), 1);
+  } else {
+    for_ids([&](int, I id) {
+      if (range_of(id) == range) atomicAdd(mine + (unsigned(id) >> shift), 1);
+    });
   }
   int base;
   block_exclusive(below, lds, &base);  // its barriers also end the counting
@@ -231,62 +245,71 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   // places: the range's rows in order, a row's tokens by wave
   int of_row = 0;
   if (int(threadIdx.x) < rows)
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) of_row += count[w * most_rows + threadIdx.x];
   int found;
   int place = base + block_exclusive(of_row, lds, &found);
-  if (int(threadIdx.x) < rows)
+  if (int(threadIdx.x) < rows) {
+    // of a run that crosses a border of pieces: the piece it ends in
+    const int first_piece = place / kPiece, last_piece = (place + of_row - 1) / kPiece;
+    if (of_row > 0 && first_piece != last_piece) a.last_piece[first_piece] = last_piece;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
       const int n = count[w * most_rows + threadIdx.x];
       count[w * most_rows + threadIdx.x] = place;
       place += n;
     }
-  if (range == ranges - 1 && threadIdx.x == 0) *a.num_sorted = base + found;
+  }
+  if (threadIdx.x == 0) {
+    if (range == ranges - 1) a.num_sorted[0] = base + found;
+    if (range == 0) a.num_sorted[1] = a.num_sorted[2] = 0;
+  }
   if (found == 0) return;
   __syncthreads();
 
-  // A wave's tokens of the range wait in a queue in LDS until there are 64 of them, so that the work on
-  // them does not grow with the tokens of other ranges.  Only this wave uses its queue and its places,
-  // and its LDS accesses stay in order.
-  __shared__ int2 queues[kSortWaves][128];  // token, row of the range
-  int2* queue = queues[wave];
-  int waiting = 0;
-  const auto place_tokens = [&](int n) {
-    const int2 q = lane < n ? queue[lane] : int2{0, 0};
-    const uint64_t active = n == 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
-    const uint64_t same = same_row(q.y, active, bits, lane);
+  // up to 64 tokens in order, one a lane
+  const auto place_tokens = [&](int n, int token, int row) {
+    const uint64_t active = n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+    const uint64_t same = same_row(row, active, bits, lane);
     if (lane < n) {
-      const int first = __hip_atomic_load(mine + q.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-      const int at = first + __popcll(same & ((uint64_t(1) << lane) - 1));
-      a.sorted_token[at] = q.x;
-      a.sorted_row[at] = int(unsigned(q.y) << shift | range);
+      const int first = __hip_atomic_load(mine + row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      const int at = first + lanes_before(same);
+      a.sorted_token[at] = token;
+      a.sorted_row[at] = int(unsigned(row) << shift | range);
       if (lane == 63 - __clzll((long long)same))  // the last of its row: the next place
-        __hip_atomic_store(mine + q.y, at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        __hip_atomic_store(mine + row, at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
   };
-  for (int64_t t0 = begin; t0 < end; t0 += 64 * kAhead) {
-    I v[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) v[j] = t0 + j * 64 + lane < end ? ids[t0 + j * 64 + lane] : I(-1);
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int64_t id = v[j];
-      const bool here = uint64_t(id) < vocab && (unsigned(id) & mask) == range;
-      const uint64_t active = __ballot(here);
-      if (active == 0) continue;
-      if (here)
-        queue[waiting + __popcll(active & ((uint64_t(1) << lane) - 1))] =
-            int2{int(t0 + j * 64 + lane), int(unsigned(id) >> shift)};
-      waiting += __popcll(active);
-      if (waiting < 64) continue;
-      __builtin_amdgcn_wave_barrier();
-      place_tokens(64);
-      waiting -= 64;
-      if (lane < waiting) queue[lane] = queue[64 + lane];
-      __builtin_amdgcn_wave_barrier();
+  if (all_listed) {
+    for (int i = 0; i < listed; i += 64) {
+      const unsigned e = i + lane < listed ? list[i + lane] : 0;
+      place_tokens(listed - i, int(first_token) + int(e >> kRowBits), int(e & ((1 << kRowBits) - 1)));
     }
+    return;
   }
+  // the list's memory as a queue of tokens that wait until there are 64
+  int2* queue = reinterpret_cast<int2*>(list);
+  static_assert(sizeof(lists[0]) >= 128 * sizeof(int2), "a queue of 128 tokens");
+  int waiting = 0;
+  const auto take = [&](int n) {
+    const int2 q = lane < n ? queue[lane] : int2{0, 0};
+    place_tokens(n, q.x, q.y);
+  };
+  for_ids([&](int t, I id) {
+    const unsigned r = range_of(id);
+    const uint64_t here = __ballot(r == range);
+    if (here == 0) return;
+    if (r == range) queue[waiting + lanes_before(here)] = int2{int(first_token) + t, int(unsigned(id) >> shift)};
+    waiting += __popcll(here);
+    if (waiting < 64) return;
+    __builtin_amdgcn_wave_barrier();
+    take(64);
+    waiting -= 64;
+    if (lane < waiting) queue[lane] = queue[64 + lane];
+    __builtin_amdgcn_wave_barrier();
+  });
   __builtin_amdgcn_wave_barrier();
-  place_tokens(waiting);
+  take(waiting);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -343,6 +366,12 @@ __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t pie
       const int next = i + 1 < cnt ? __builtin_amdgcn_readlane(rows, i + 1) : after;
       if (next == row && i + 1 < cnt) continue;
       if (n > 0) {
+        if (!open && next == row && c == 0) {  // short runs from the front of the list, long ones from its end
+          const int last = a.last_piece[piece], pieces = int(ceil_div(a.tokens, kPiece));
+          const int at = last - piece < kShortRun ? atomicAdd(a.num_sorted + 1, 1)
+                                                  : pieces - 1 - atomicAdd(a.num_sorted + 2, 1);
+          a.runs[at] = EmbeddingRun{int(piece), last, row};
+        }
         if (open || next == row)
           store_vec<float, E, false, kWhole>(a.partial + (2 * piece + (open ? 0 : 1)) * a.dim + c, n, acc);
         else
@@ -359,7 +388,7 @@ __device__ __forceinline__ void sum_piece(const EmbeddingBwdArgs& a, int64_t pie
 template <typename T, bool kWhole>
 __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArgs a) {
   constexpr int E = kVec<T>;
-  const int total = *a.num_sorted;
+  const int total = a.num_sorted[0];
   const int64_t chunks = ceil_div(a.dim, 64 * E), items = ceil_div(total, kPiece) * chunks;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   for (int64_t item = int64_t(blockIdx.x) * 4 + wave; item < items; item += int64_t(gridDim.x) * 4) {
@@ -368,65 +397,80 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingBwdArg
   }
 }
 
-// Adds the partial sums of a run that begins in a piece and ends in a later one: a workgroup takes 64
-// vectors of columns, its waves a quarter of the run's pieces each, in order; the quarters meet in LDS.
+// Sum of the partial sums of pieces q0 to q1 - 1 of a run that begins in `piece`, in order.
+template <int E, bool kWhole>
+__device__ __forceinline__ void sum_partials(const EmbeddingBwdArgs& a, int64_t piece, int64_t q0, int64_t q1,
+                                             int64_t c, int n, float (&acc)[E]) {
+  constexpr int kAhead = 64 / E;
+  for (int64_t q = q0; q < q1; q += kAhead) {
+    const float* from[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t p = q + j < q1 ? q + j : q1 - 1;
+      from[j] = a.partial + (2 * p + (p == piece ? 1 : 0)) * a.dim;
+    }
+    Raw<float, E> r[kAhead];
+    load_vecs<float, E, kAhead, false, kWhole>(r, from, c, n, a.dim >= E);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (q + j < q1) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[k] += r[j].get(k);
+      }
+  }
+}
+
+// Adds the partial sums of the runs that begin in a piece and end in a later one, 64 vectors of columns
+// at a time.  Most runs are of a few pieces: a wave's task.  The others are shared by a workgroup's waves,
+// an equal part of the run's pieces each, in order; the parts meet in LDS.  The time is a chain of waits
+// (the count and a run, then its partial sums in turns), so all tasks have to run at once.
+constexpr int kJoinWaves = 8;
+constexpr int kJoinLongWgs = 32;
+constexpr int kJoinShortWgs = 96;
 template <typename T, bool kWhole>
-__global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingBwdArgs a) {
-  constexpr int E = kVec<T>, kAhead = 64 / E;
-  __shared__ float quarter[3][64 * E];
+__global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(EmbeddingBwdArgs a) {
+  constexpr int E = kVec<T>;
+  __shared__ float part[kJoinWaves - 1][64 * E];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int total = *a.num_sorted;
-  const int64_t last_border = (int64_t(total) - 1) / kPiece;  // pieces 0 .. last_border hold tokens
-  for (int64_t piece = blockIdx.x; piece < last_border; piece += gridDim.x) {
-    const int64_t border = (piece + 1) * kPiece, begin = piece * kPiece;
-    // read together: a wait for each would cost more
-    const int row = a.sorted_row[border], inner = a.sorted_row[border - 1];
-    const int before = a.sorted_row[begin > 0 ? begin - 1 : 0];
-    if (inner != row || (begin > 0 && before == row)) continue;  // no run crosses here, or it begins earlier
-    // the run goes on while pieces begin with its row; 64 pieces are looked at at a time
-    int64_t next = piece + 2;
-    for (;; next += 64) {
-      const int64_t p = next + lane;
-      const uint64_t ended = __ballot(p > last_border || a.sorted_row[p * kPiece] != row);
-      if (ended != 0) {
-        next += __ffsll((unsigned long long)ended) - 1;
-        break;
+  const int pieces = int(ceil_div(a.tokens, kPiece));
+  const int64_t step = int64_t(gridDim.y) * 64 * E;
+  if (blockIdx.x >= kJoinLongWgs) {
+    const int first = int(blockIdx.x - kJoinLongWgs) * kJoinWaves + wave;
+    const int runs = a.num_sorted[1];
+    for (int k = first; k < runs; k += kJoinShortWgs * kJoinWaves) {
+      const EmbeddingRun run = a.runs[k];
+      for (int64_t c0 = int64_t(blockIdx.y) * 64 * E; c0 < a.dim; c0 += step) {
+        const int64_t c = c0 + lane * E;
+        const int n = tail<E>(a.dim - c);
+        float acc[E] = {};
+        sum_partials<E, kWhole>(a, run.first, run.first, int64_t(run.last) + 1, c, n, acc);
+        if (n > 0) write_row<T, E, kWhole>(a, run.row, c, n, acc);
       }
     }
-    const int64_t pieces = next - piece, share = ceil_div(pieces, 4);
-    const int64_t q0 = piece + wave * share, q1 = q0 + share < piece + pieces ? q0 + share : piece + pieces;
-    for (int64_t c0 = int64_t(blockIdx.y) * 64 * E; c0 < a.dim; c0 += int64_t(gridDim.y) * 64 * E) {
+    return;
+  }
+  const int runs = a.num_sorted[2];
+  for (int k = blockIdx.x; k < runs; k += kJoinLongWgs) {
+    const EmbeddingRun run = a.runs[pieces - 1 - k];
+    const int64_t end = int64_t(run.last) + 1, share = ceil_div(end - run.first, kJoinWaves);
+    const int64_t q0 = run.first + wave * share, q1 = q0 + share < end ? q0 + share : end;
+    for (int64_t c0 = int64_t(blockIdx.y) * 64 * E; c0 < a.dim; c0 += step) {
       const int64_t c = c0 + lane * E;
       const int n = tail<E>(a.dim - c);
       float acc[E] = {};
-      for (int64_t q = q0; q < q1; q += kAhead) {
-        const float* from[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int64_t p = q + j < q1 ? q + j : q1 - 1;
-          from[j] = a.partial + (2 * p + (p == piece ? 1 : 0)) * a.dim;
-        }
-        Raw<float, E> r[kAhead];
-        load_vecs<float, E, kAhead, false, kWhole>(r, from, c, n, a.dim >= E);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (q + j < q1) {
-#pragma unroll
-            for (int k = 0; k < E; ++k) acc[k] += r[j].get(k);
-          }
-      }
-      __syncthreads();  // the last columns' quarters are read
+      sum_partials<E, kWhole>(a, run.first, q0, q1, c, n, acc);
+      __syncthreads();  // the last columns' parts are read
       if (wave > 0) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) quarter[wave - 1][k * 64 + lane] = acc[k];
+        for (int j = 0; j < E; ++j) part[wave - 1][j * 64 + lane] = acc[j];
       }
       __syncthreads();
       if (wave == 0 && n > 0) {
 #pragma unroll
-        for (int w = 0; w < 3; ++w)
+        for (int w = 0; w < kJoinWaves - 1; ++w)
 #pragma unroll
-          for (int k = 0; k < E; ++k) acc[k] += quarter[w][k * 64 + lane];
-        write_row<T, E, kWhole>(a, row, c, n, acc);
+          for (int j = 0; j < E; ++j) acc[j] += part[w][j * 64 + lane];
+        write_row<T, E, kWhole>(a, run.row, c, n, acc);
       }
     }
   }
@@ -505,12 +549,19 @@ __global__ __launch_bounds__(kThreads) void embedding_zero_kernel(T* table, int6
     store_vec<T, E, false, false>(table + e, tail<E>(n - e), none);
 }
 
+// Up to so many bytes the zeros are written beside the sort: 76 MB with 50021 tokens 84 us instead of 90 in
+// a launch of its own, 156 MB with 8192 tokens 56 instead of 58.  Beyond, the shorter-lived workgroups of
+// a launch of its own gain more: 500 MB 122 us instead of 127, 1 GB 202 instead of 214.
+constexpr int64_t kZeroBesideSort = int64_t(256) << 20;
+
 template <typename T, typename I, bool kWhole>
 void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
-  if (a.tokens <= kDirectTokens) {
-    if (!a.accumulate)
-      hipLaunchKernelGGL((embedding_zero_kernel<T>), dim3(grid_of(a.vocab * a.dim, kThreads * kVec<T>)), dim3(kThreads),
-                         0, s, static_cast<T*>(a.dtable), a.vocab * a.dim);
+  const int64_t elems = a.accumulate ? 0 : a.vocab * a.dim;
+  const bool direct = a.tokens <= kDirectTokens, zero_first = direct || elems * int64_t(sizeof(T)) > kZeroBesideSort;
+  if (zero_first && elems > 0)
+    hipLaunchKernelGGL((embedding_zero_kernel<T>), dim3(grid_of(elems, kThreads * kVec<T>)), dim3(kThreads), 0, s,
+                       static_cast<T*>(a.dtable), elems);
+  if (direct) {
     if (a.tokens > 0)
       hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
     return;
@@ -520,13 +571,15 @@ void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
   int bits = 0;
   while ((1 << bits) < rows) ++bits;
   const unsigned sorting = unsigned(a.vocab < ranges ? a.vocab : ranges);
-  const unsigned zeroing = a.accumulate ? 0 : grid_of(a.vocab * a.dim, kSortThreads * kVec<T>);
+  const unsigned zeroing = zero_first || elems == 0 ? 0 : grid_of(elems, kSortThreads * kVec<T>);
   hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(sorting + zeroing), dim3(kSortThreads),
                      kSortWaves * rows * sizeof(int), s, a, sorting, shift, int(rows), bits);
   const int64_t pieces = ceil_div(a.tokens, kPiece), chunks = ceil_div(ceil_div(a.dim, kVec<T>), 64);
   hipLaunchKernelGGL((embedding_sum_kernel<T, kWhole>), dim3(grid_of(pieces * chunks, 4)), dim3(kThreads), 0, s, a);
-  hipLaunchKernelGGL((embedding_join_kernel<T, kWhole>), dim3(grid_of(pieces - 1, 1), unsigned(chunks < 64 ? chunks : 64)),
-                     dim3(kThreads), 0, s, a);
+  // how many runs there are is known on the device only
+  hipLaunchKernelGGL((embedding_join_kernel<T, kWhole>),
+                     dim3(kJoinLongWgs + kJoinShortWgs, unsigned(chunks < 64 ? chunks : 64)), dim3(kJoinWaves * 64), 0,
+                     s, a);
 }
 template <typename T, typename I>
 void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {

@@ -122,7 +122,11 @@ inline int sort_shift(int64_t vocab) {
 // Sorted tokens are summed in pieces of kPiece.  A run of equal ids that crosses a border of pieces
 // leaves fp32 partial sums, at most two for each piece, that a second kernel adds in order.
 constexpr int kPiece = 32;
+constexpr int kShortRun = 16;  // pieces of a run that one wave adds
 
+struct EmbeddingRun {
+  int32_t first, last, row;  // pieces, and the table's row
+};
 struct EmbeddingBwdArgs {
   int64_t tokens, vocab, dim;
   const void* ids;
@@ -132,7 +136,9 @@ struct EmbeddingBwdArgs {
   void* dtable;
   int32_t* sorted_token;  // [tokens]
   int32_t* sorted_row;    // [tokens]
-  int32_t* num_sorted;    // tokens inside the table
+  int32_t* num_sorted;    // [3]: tokens inside the table, short and long runs that cross a border of pieces
+  int32_t* last_piece;    // [pieces]: where such a run begins, the piece it ends in
+  EmbeddingRun* runs;     // [pieces]: such runs in any order, the long ones from the end on
   float* partial;         // [pieces][2][dim]
 };
 int launch_embedding_bwd(const EmbeddingBwdArgs& a, int dtype, int ids_dtype, void* stream);
