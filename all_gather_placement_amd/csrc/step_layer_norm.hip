@@ -389,6 +389,109 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_rows_kernel(Lay
   }
 }
 
+// Few rows: one launch without partial sums.  Workgroups below `row_wgs` make a row of dx each; the
+// others read all rows of 64 vectors of columns again, four waves every fourth row, and write the
+// parameters' gradients.
+constexpr int kColWaves = 4;
+template <typename T, typename PT, int NV, bool kWhole>
+__global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_few_kernel(LayerNormBwdArgs a, unsigned row_wgs) {
+  constexpr int E = kVec<T>;
+  const int D = int(a.cols), wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (blockIdx.x < row_wgs) {
+    __shared__ float lds[2 * kMaxWaves];
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    const float mean = a.mean[row], rstd = a.rstd[row], inv = 1.0f / float(D);
+    Raw<T, E> rx[NV], rd[NV];
+    Raw<PT, E> rw[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E;
+      rx[v] = load_vec<T, E, false, kWhole>(x + c, D - c, D >= E);
+      rd[v] = load_vec<T, E, false, kWhole>(dy + c, D - c, D >= E);
+      if (a.weight != nullptr) rw[v] = load_vec<PT, E, false, kWhole>(static_cast<const PT*>(a.weight) + c, D - c, D >= E);
+    }
+    float s[2] = {0, 0};
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int n = D - (v * int(blockDim.x) + int(threadIdx.x)) * E;
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float xhat = k < n ? (rx[v].get(k) - mean) * rstd : 0.0f;
+        const float g = a.weight != nullptr ? rd[v].get(k) * rw[v].get(k) : rd[v].get(k);
+        s[0] += g;
+        s[1] += g * xhat;
+      }
+    }
+    block_sums<2>(s, lds);
+    const float m1 = s[0] * inv, m2 = s[1] * inv;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * int(blockDim.x) + int(threadIdx.x)) * E, n = D - c;
+      if (n <= 0) continue;
+      float o[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float xhat = (rx[v].get(k) - mean) * rstd;
+        const float g = a.weight != nullptr ? rd[v].get(k) * rw[v].get(k) : rd[v].get(k);
+        o[k] = rstd * (g - m1 - xhat * m2);
+      }
+      store_vec<T, E, false, kWhole>(static_cast<T*>(a.dx) + row * a.dx_stride + c, n, o);
+    }
+    return;
+  }
+  constexpr int kAhead = 8;
+  __shared__ float part[kColWaves - 1][2 * 64 * E];
+  const int waves = int(blockDim.x >> 6) < kColWaves ? int(blockDim.x >> 6) : kColWaves;
+  const int c = (int(blockIdx.x - row_wgs) * 64 + lane) * E, n = D - c, rows = int(a.rows);
+  float dw[E] = {}, db[E] = {};
+  if (wave < waves) {
+    for (int r0 = wave; r0 < rows; r0 += waves * kAhead) {
+      Raw<T, E> rx[kAhead], rd[kAhead];
+      float mean[kAhead], rstd[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t row = r0 + j * waves < rows ? r0 + j * waves : rows - 1;
+        rx[j] = load_vec<T, E, false, kWhole>(static_cast<const T*>(a.x) + row * a.x_stride + c, n, D >= E);
+        rd[j] = load_vec<T, E, false, kWhole>(static_cast<const T*>(a.dy) + row * a.dy_stride + c, n, D >= E);
+        mean[j] = a.mean[row];
+        rstd[j] = a.rstd[row];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (r0 + j * waves >= rows) break;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          dw[k] += rd[j].get(k) * ((rx[j].get(k) - mean[j]) * rstd[j]);
+          db[k] += rd[j].get(k);
+        }
+      }
+    }
+    if (wave > 0) {
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        part[wave - 1][k * 64 + lane] = dw[k];
+        part[wave - 1][(E + k) * 64 + lane] = db[k];
+      }
+    }
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  for (int w = 1; w < waves; ++w) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      dw[k] += part[w - 1][k * 64 + lane];
+      db[k] += part[w - 1][(E + k) * 64 + lane];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    if (k < n && a.dweight != nullptr) static_cast<PT*>(a.dweight)[c + k] = narrow<PT>(dw[k]);
+    if (k < n && a.dbias != nullptr) static_cast<PT*>(a.dbias)[c + k] = narrow<PT>(db[k]);
+  }
+}
+
 // Rows wider than the registers: the input's gradient, two passes over a row.
 template <typename T, typename PT>
 __global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_wide_kernel(LayerNormBwdArgs a) {
@@ -548,6 +651,10 @@ void with_form(int64_t bytes, int64_t cols, F&& f) {
   });
 }
 
+// The backward pass of up to so many rows is one launch: 16 rows of 4096 bf16 3.6 us, with partial sums
+// and their join 7.2; 16 rows of 1001 6.9 and 7.4; 64 rows of 1001 would take 21 instead of 8.
+constexpr int kFewRows = 16;
+
 template <typename T, typename PT>
 void forward(const LayerNormArgs& a, hipStream_t s) {
   const int64_t vecs = ceil_div(a.cols, kVec<T>);
@@ -577,6 +684,27 @@ template <typename T, typename PT>
 void backward(LayerNormBwdArgs a, int groups, hipStream_t s) {
   const bool params = a.dweight != nullptr || a.dbias != nullptr;
   const int64_t vecs = ceil_div(a.cols, kVec<T>);
+  if (params && a.rows > 0 && a.rows <= kFewRows && vecs <= 64 * kMaxWaves * 2) {
+    with_whole<kVec<T>>(a.cols, [&](auto w) {
+      constexpr bool whole = decltype(w)::value;
+      const unsigned rows = a.dx != nullptr ? unsigned(a.rows) : 0, cols = unsigned(ceil_div(vecs, 64));
+      const auto launch = [&](unsigned row_wgs, unsigned col_wgs) {
+        if (vecs <= 64 * kMaxWaves)
+          hipLaunchKernelGGL((layer_norm_bwd_few_kernel<T, PT, 1, whole>), dim3(row_wgs + col_wgs), dim3(cols * 64), 0, s,
+                             a, row_wgs);
+        else
+          hipLaunchKernelGGL((layer_norm_bwd_few_kernel<T, PT, 2, whole>), dim3(row_wgs + col_wgs),
+                             dim3(ceil_div(vecs, 128) * 64), 0, s, a, row_wgs);
+      };
+      if (a.dx == a.dy) {  // the sums first: they read dy too
+        launch(0, cols);
+        launch(rows, 0);
+      } else {
+        launch(rows, cols);
+      }
+    });
+    return;
+  }
   if (!params) a.partial = nullptr;
   if (a.rows > 0)
     with_form<kVec<T>>(3 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {

@@ -113,6 +113,26 @@ def test_rows_end_where_they_end(gpu_available, cols, dtype):
     assert torch.equal(grad[2], dy0[0]) and int(torch.count_nonzero(grad[[0, 1, 3]])) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=str)
+@pytest.mark.parametrize("cols", [2, 40, 63, 130, 300, 1001, 4096, 8192, 8203, 16384])
+@pytest.mark.parametrize("rows", [15, 16, 17, 33])
+def test_layer_norm_bwd_around_few_rows(gpu_available, rows, cols, dtype):
+    say("layer norm gradient of few rows", rows, cols, dtype)
+
+    def among_nan(values):
+        buf = torch.full((rows, cols + 2), float("nan"), dtype=values.dtype, device="cuda")
+        buf[:, 1:-1] = values
+        return buf[:, 1:-1]
+
+    x, dy = normal((rows, cols), dtype, cols, 2.0), normal((rows, cols), dtype, 7)
+    w = normal((cols,), FP32, 1, 0.2, 1.0)
+    want = check_ln_bwd(among_nan(dy), among_nan(x), w)
+    _, mean, rstd = layer_norm(x, w)
+    inplace = dy.clone()
+    got = layer_norm_bwd(inplace, x, w, mean, rstd, dx=inplace)
+    assert got[0] is inplace and all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 # ------------------------------------------------------------------------------------------------
 # Gradient norm and clipping
 # ------------------------------------------------------------------------------------------------
