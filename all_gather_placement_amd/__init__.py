@@ -5,7 +5,8 @@ marshals arguments to it.  Importing the package does not load the library; the 
 and fails loudly if it has not been built (``python -m all_gather_placement_amd.build``).
 
 ``libtide_step.so`` holds the training-step operators on either side of the collectives (gradient norm
-and clipping, layer norm, embedding, with their gradients); they are bound in :mod:`.step`.
+and clipping, layer norm, embedding, with their gradients); they are bound in :mod:`.step` and its
+compiled module ``_step.so``.
 """
 from .step import (  # noqa: F401
     clip_grad_norm,

@@ -6,13 +6,16 @@
 //
 // HBM bounds both directions: a row is read once into registers, where the mean and then the
 // centred squares are summed in fp32 (two passes over registers, so a large mean costs no digits),
-// and written once.  A row belongs to a group of L lanes that hold NV vectors of eight elements
-// each; a group is part of a wave for narrow rows and a workgroup for wide ones.  Rows too wide for
-// the registers are streamed instead, and read again from the caches.
+// and written once.  A lane holds 16-byte vectors; a row belongs to a part of a wave, to a wave or to
+// the waves of a workgroup.  Rows too wide for the registers are streamed instead, and read again from
+// the caches.
 //
 // The parameter gradients are sums down the columns: each workgroup keeps the sums of its rows in
 // registers, in row order, and leaves them in the workspace; a second kernel adds the workgroups'
-// sums in order.
+// sums in a fixed order.
+//
+// Measured: 32760 x 5120 bf16 forward 114 us (5.9 TB/s; a copy of the same bytes takes 109), 8192 x 8192
+// bf16 backward 72 us and 6 of the second kernel (437 MB move in the first, 6.1 TB/s).
 #include "step_device.h"
 #include "step_internal.h"
 
@@ -614,7 +617,7 @@ void with_lanes(int64_t vecs, F&& f) {
 //
 // Forward: three vectors a lane and two rows a workgroup keep about 16 waves with 60 KiB of loads in
 // flight on a compute unit and halve the reads of weight and bias (32760 x 5120 bf16: 113 us; two
-// vectors 122, four 119, one row 122, ten vectors in one wave without barriers 133; a copy of the same
+// vectors 122, four 119, one row 122, ten vectors in one wave, without a barrier, 146; a copy of the same
 // bytes takes 109).  Few rows go to as many waves as they fill: the time is one row's.
 template <typename F>
 bool with_rows(int64_t vecs, int64_t rows, F&& f) {

@@ -8,9 +8,9 @@
 // nothing).  Each workgroup leaves one partial sum, and the partial sums are added in order, so the
 // result depends on the sizes alone.
 //
-// Measured: 391 bf16 tensors of 3 MiB, 1.23 GB, in 196 us with both launches and the finish (6.3 TB/s;
-// 7.1 is what reading alone reaches); 64 fp32 tensors, 1.4 GB, summed in 205 us and clipped in 440 us
-// (6.4 TB/s, the rate of a copy).  The sum reads past the caches: with plain loads the call takes 712 us
+// Measured: 391 bf16 tensors of 3 MiB, 1.23 GB, in 186 us with both launches and the finish (6.6 TB/s;
+// 7.1 is what reading alone reaches); 64 fp32 tensors, 1.4 GB, summed in 205 us and clipped in 440 to 455 us
+// (6.2 to 6.4 TB/s, the rate of a copy).  The sum reads past the caches: with plain loads the call takes 712 us
 // instead of 667, and leaving the last 96 or 192 MiB in the caches for the clipping 713 or 734.
 #include "step_device.h"
 #include "step_internal.h"
