@@ -201,7 +201,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   for (int i = threadIdx.x; i < kSortWaves * most_rows; i += kSortThreads) count[i] = 0;
 
   // each wave reads a part of the tokens of its own, in order
-  constexpr int kAhead = 16;  // loads in flight
+  constexpr int kAhead = 16;  // loads in flight (32 take more than 64 registers: fewer workgroups write zeros)
   const int64_t part = ceil_div(ceil_div(a.tokens, kSortWaves), 64) * 64;
   const int64_t first_token = __builtin_amdgcn_readfirstlane(wave) * part;
   const int end = int(first_token + part < a.tokens ? part : a.tokens > first_token ? a.tokens - first_token : 0);
@@ -209,8 +209,13 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   const auto for_ids = [&](auto&& f) {  // f(token of the part, id), all lanes together; id -1 beyond the end
     for (int t0 = 0; t0 < end; t0 += 64 * kAhead) {
       I v[kAhead];
+      if (end - t0 >= 64 * kAhead) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) v[j] = lane + j * 64 < end - t0 ? from[t0 + (lane + j * 64)] : I(-1);
+        for (int j = 0; j < kAhead; ++j) v[j] = from[t0 + (lane + j * 64)];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j] = lane + j * 64 < end - t0 ? from[t0 + (lane + j * 64)] : I(-1);
+      }
       loads_first();
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) f(t0 + j * 64 + lane, v[j]);
