@@ -134,27 +134,36 @@ int64_t norm_workspace(int32_t n, const int64_t* numels, int dtype) {
   return 16 + (num_partials(n, numels, dtype) * 8 + 15) / 16 * 16;
 }
 
-int enqueue_norm(int32_t n, const void* const* grads, const int64_t* numels, int dtype, double* sumsq, float* norm,
-                 void* workspace, void* stream) {
-  double* partial = static_cast<double*>(workspace) + 2;
-  const bool one = one_workgroup(num_chunks(n, numels, dtype));
-  int used = 0;
-  const int e = for_tables<NormTable, kNormBatch>(
+// The partial sums of squares, `used` of them from workspace + 16 bytes on; one workgroup's calls write
+// the results themselves.
+int enqueue_partials(int32_t n, const void* const* grads, const int64_t* numels, int dtype, double* sumsq, float* norm,
+                     double* partial, bool one, int* used, void* stream) {
+  *used = 0;
+  return for_tables<NormTable, kNormBatch>(
       n, numels, dtype, [&](NormEntry& t, int32_t i) { t.p = grads[i]; },
       [&](NormTable& t) {
         const int grid = one ? 1 : norm_grid(t.chunks);
         t.sumsq = one ? sumsq : nullptr;
         t.norm = one ? norm : nullptr;
-        const int err = launch_norm_partial(t, dtype, partial + used, grid, stream);
-        used += grid;
+        const int err = launch_norm_partial(t, dtype, partial + *used, grid, stream);
+        *used += grid;
         return err;
       });
+}
+int enqueue_norm(int32_t n, const void* const* grads, const int64_t* numels, int dtype, double* sumsq, float* norm,
+                 void* workspace, void* stream) {
+  double* partial = static_cast<double*>(workspace) + 2;
+  const bool one = one_workgroup(num_chunks(n, numels, dtype));
+  int used;
+  const int e = enqueue_partials(n, grads, numels, dtype, sumsq, norm, partial, one, &used, stream);
   return e != 0 ? e : launch_norm_finish(partial, used, one ? nullptr : sumsq, one ? nullptr : norm, stream);
 }
 
-// Clipping by *sumsq, or, where `sum_to` is given, one workgroup's sum and clipping by it.
+// Clipping by *sumsq; or, where `sum_to` is given, by the sum of `partials` partial sums, or of one
+// workgroup's own, which is written there.
 int enqueue_clip(int32_t n, const void* const* grads, void* const* outs, const int64_t* numels, int dtype,
-                 const double* sumsq, double* sum_to, double max_norm, float* norm, void* stream) {
+                 const double* sumsq, double* sum_to, const double* partial, int partials, double max_norm, float* norm,
+                 void* stream) {
   bool first = true;
   const int e = for_tables<ClipTable, kClipBatch>(
       n, numels, dtype,
@@ -164,7 +173,9 @@ int enqueue_clip(int32_t n, const void* const* grads, void* const* outs, const i
       },
       [&](ClipTable& t) {
         t.sum_to = sum_to;
-        const int grid = sum_to != nullptr ? 1 : clip_grid(t.chunks);
+        t.partial = partial;
+        t.partials = partials;
+        const int grid = sum_to != nullptr && partial == nullptr ? 1 : clip_grid(t.chunks);
         const int err = launch_clip(t, dtype, sumsq, max_norm, first ? norm : nullptr, grid, stream);
         first = false;
         return err;
@@ -174,6 +185,8 @@ int enqueue_clip(int32_t n, const void* const* grads, void* const* outs, const i
   none.count = 0;
   none.chunks = 0;
   none.sum_to = nullptr;
+  none.partial = nullptr;
+  none.partials = 0;
   return launch_clip(none, dtype, sumsq, max_norm, norm, 1, stream);
 }
 
@@ -246,7 +259,7 @@ tide_status tide_grad_clip(int32_t num_tensors, const void* const* grads, void* 
   std::vector<Range> scalars{range_of(sumsq, 8)};
   if (norm != nullptr) scalars.push_back(range_of(norm, 4));
   if (clip_overlaps(num_tensors, grads, outs, numels, dtype, scalars)) return TIDE_ERR_INVALID;
-  return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, sumsq, nullptr, max_norm, norm, stream));
+  return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, sumsq, nullptr, nullptr, 0, max_norm, norm, stream));
 } catch (const std::bad_alloc&) {
   return TIDE_ERR_NOMEM;
 }
@@ -265,10 +278,21 @@ tide_status tide_clip_grad_norm(int32_t num_tensors, const void* const* grads, v
   if (norm != nullptr) scalars.push_back(range_of(norm, 4));
   if (clip_overlaps(num_tensors, grads, outs, numels, dtype, scalars)) return TIDE_ERR_INVALID;
   double* s = sumsq != nullptr ? sumsq : static_cast<double*>(workspace);
-  if (one_workgroup(num_chunks(num_tensors, numels, dtype)))
-    return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, s, s, max_norm, norm, stream));
-  int e = enqueue_norm(num_tensors, grads, numels, dtype, s, norm, workspace, stream);
-  if (e == 0) e = enqueue_clip(num_tensors, grads, outs, numels, dtype, s, nullptr, max_norm, nullptr, stream);
+  const int64_t chunks = num_chunks(num_tensors, numels, dtype);
+  if (one_workgroup(chunks))
+    return status_of(
+        enqueue_clip(num_tensors, grads, outs, numels, dtype, s, s, nullptr, 0, max_norm, norm, stream));
+  int e;
+  if (chunks > 0 && chunks <= kNormClipAddsChunks && num_tensors <= kClipBatch) {
+    double* partial = static_cast<double*>(workspace) + 2;
+    int used;
+    e = enqueue_partials(num_tensors, grads, numels, dtype, nullptr, nullptr, partial, false, &used, stream);
+    if (e == 0)
+      e = enqueue_clip(num_tensors, grads, outs, numels, dtype, s, s, partial, used, max_norm, norm, stream);
+  } else {
+    e = enqueue_norm(num_tensors, grads, numels, dtype, s, norm, workspace, stream);
+    if (e == 0) e = enqueue_clip(num_tensors, grads, outs, numels, dtype, s, nullptr, nullptr, 0, max_norm, nullptr, stream);
+  }
   return status_of(e);
 } catch (const std::bad_alloc&) {
   return TIDE_ERR_NOMEM;

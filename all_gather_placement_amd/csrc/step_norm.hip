@@ -189,6 +189,39 @@ __global__ __launch_bounds__(kNormThreads) void clip_kernel(ClipTable t, const d
   }
 }
 
+// As norm_finish_kernel, to the bit: a wave adds 64 neighbouring partial sums, the waves' sums follow in
+// order.
+__device__ __forceinline__ double add_partials(const double* __restrict__ partial, int n) {
+  constexpr int kParts = kOneWgThreads / kNormThreads, kWaves = kNormThreads / 64;
+  static_assert(kNormWgs <= kOneWgThreads, "one partial sum for each thread of norm_finish_kernel");
+  __shared__ double lds[kParts * kWaves];
+#pragma unroll
+  for (int j = 0; j < kParts; ++j) {
+    const int k = j * kNormThreads + int(threadIdx.x);
+    const double v = wave_sum(k < n ? partial[k] : 0.0);
+    if ((threadIdx.x & 63) == 0) lds[j * kWaves + threadIdx.x / 64] = v;
+  }
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int w = 0; w < kParts * kWaves; ++w) s += lds[w];
+  return s;
+}
+
+// Few chunks: a workgroup for each, which adds up the partial sums itself; a launch less.
+template <typename T>
+__global__ __launch_bounds__(kNormThreads) void clip_adding_kernel(ClipTable t, double max_norm,
+                                                                   float* __restrict__ norm) {
+  const double s = add_partials(t.partial, t.partials);
+  if (blockIdx.x == 0) write_norm(s, t.sum_to, norm);
+  const float coef = clip_coef(sqrt(s), max_norm);
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const Chunk k = chunk_of<T>(t, c, entry_of(t, c));
+    scale_chunk<T, 4, false>(static_cast<const T*>(t.e[k.entry].p) + k.at, static_cast<T*>(t.e[k.entry].out) + k.at,
+                             k.n, threadIdx.x, coef);
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(kOneWgThreads) void clip_one_kernel(ClipTable t, double max_norm,
                                                                  float* __restrict__ norm) {
@@ -227,7 +260,9 @@ int launch_norm_finish(const double* partial, int n, double* sumsq, float* norm,
 
 template <typename T>
 static int clip(const ClipTable& t, const double* sumsq, double max_norm, float* norm, int grid, hipStream_t s) {
-  if (t.sum_to != nullptr)
+  if (t.partial != nullptr)
+    hipLaunchKernelGGL(clip_adding_kernel<T>, dim3(grid), dim3(kNormThreads), 0, s, t, max_norm, norm);
+  else if (t.sum_to != nullptr)
     hipLaunchKernelGGL(clip_one_kernel<T>, dim3(1), dim3(kOneWgThreads), 0, s, t, max_norm, norm);
   else
     hipLaunchKernelGGL(clip_kernel<T>, dim3(grid * kClipParts), dim3(kNormThreads), 0, s, t, sumsq, max_norm, norm);
