@@ -15,8 +15,8 @@
 // cross pieces, in a fixed order.
 //
 // Measured: lookup of 65536 rows of 4096 bf16 128 us; gradient of 8192 such rows in a table of 131072
-// 201 us (zeros 157, sort 9, sums 23, join 6), of 50021 rows of 1001 fp32 in 20011 77 us (sort beside the
-// zeros 21, sums 48 -- 5.1 TB/s, rows at 4-byte boundaries --, join 7).
+// 200 us (zeros 160, sort 8, sums 23, join 6), of 50021 rows of 1001 fp32 in 20011 75 us (sort beside the
+// zeros 20, sums 48 -- 5.1 TB/s, rows at 4-byte boundaries --, join 7).
 #include "step_device.h"
 #include "step_internal.h"
 
@@ -178,7 +178,7 @@ __device__ __forceinline__ uint64_t same_row(int row, uint64_t active, int bits,
 // 157 us, 1024 threads 169, a wave for each row 194).  Rows that have tokens are written again by the
 // sums, which costs less than asking for each row whether it has any (237 us with the sums, 30 more).
 //
-// 50021 tokens of a text over 20011 rows: 21 us; with the ids read once more for the places 24, without
+// 50021 tokens of a text over 20011 rows: 20 us; with the ids read once more for the places 24, without
 // a queue or list, a few tokens at a time, 28, and with a row's lanes found by all of its bits 44.
 template <typename T, typename I>
 __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingBwdArgs a, unsigned ranges, int shift,
@@ -487,7 +487,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(Embeddi
 }
 
 // Few tokens: a workgroup for each, which looks at all ids, goes on if its own is the first of its row,
-// and sums the row's tokens in ascending order.
+// and sums the row's tokens, in ascending order or in ascending quarters.
 template <typename T, typename I, bool kWhole>
 __global__ __launch_bounds__(kThreads) void embedding_direct_kernel(EmbeddingBwdArgs a) {
   constexpr int E = kVec<T>, kAhead = 16, kMasks = kDirectTokens / 64;
@@ -528,13 +528,20 @@ __global__ __launch_bounds__(kThreads) void embedding_direct_kernel(EmbeddingBwd
   }
   __syncthreads();
   const int n = before[kMasks];
-  // a wave takes 64 vectors of columns; all of its lanes go along, those beyond the last column too
-  for (int64_t c0 = int64_t(threadIdx.x / 64) * 64 * E; c0 < a.dim; c0 += kThreads * E) {
+  // A wave takes 64 vectors of columns; all of its lanes go along, those beyond the last column too.  Rows
+  // of no more than that are shared: each wave adds a quarter of the tokens.
+  constexpr int kWaves = kThreads / 64;
+  __shared__ float part[kWaves - 1][64 * E];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool shared = a.dim <= 64 * E;
+  const int share = shared ? (n + kWaves - 1) / kWaves : n;
+  const int t0 = shared ? wave * share : 0, t1 = t0 + share < n ? t0 + share : n;
+  for (int64_t c0 = shared ? 0 : int64_t(wave) * 64 * E; c0 < a.dim; c0 += kThreads * E) {
     const int64_t c = c0 + lane * E;
     const int m = tail<E>(a.dim - c);
     float acc[E] = {};
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-      const int token = list[i0 + lane < n ? i0 + lane : n - 1];
+    for (int i0 = t0; i0 < t1; i0 += kAhead) {
+      const int token = list[i0 + lane < t1 ? i0 + lane : t1 - 1];
       const T* from[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
@@ -543,10 +550,22 @@ __global__ __launch_bounds__(kThreads) void embedding_direct_kernel(EmbeddingBwd
       load_vecs<T, E, kAhead, true, kWhole>(r, from, c, m, a.dim >= E);
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        if (i0 + j < n) {
+        if (i0 + j < t1) {
 #pragma unroll
           for (int k = 0; k < E; ++k) acc[k] += r[j].get(k);
         }
+    }
+    if (shared) {  // one turn of the loop
+      if (wave > 0) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) part[wave - 1][k * 64 + lane] = acc[k];
+      }
+      __syncthreads();
+      if (wave > 0) return;
+#pragma unroll
+      for (int w = 0; w < kWaves - 1; ++w)
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[k] += part[w][k * 64 + lane];
     }
     if (m > 0) write_row<T, E, kWhole>(a, int(row), c, m, acc);
   }

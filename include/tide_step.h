@@ -145,8 +145,8 @@ tide_status tide_embedding(int64_t tokens, const void* ids, int32_t ids_dtype, i
  *   accumulate    0: dtable is written, zero rows included; 1: the gradient is added to it (a table
  *                 that is also the output projection, gradients summed over micro-batches)
  * Result: dtable[v] = scale * (sum of dy[t] over the t with ids[t] = v) [+ the old dtable[v]], in
- * fp32, rounded once.  Tokens of equal id are brought together in ascending t and summed in that
- * order within pieces of fixed length, the pieces' sums in a fixed order.  With accumulate, rows of no token are
+ * fp32, rounded once.  The tokens of a row are taken in ascending t and summed in parts, the parts' sums
+ * in an order that is fixed for given ids and sizes.  With accumulate, rows of no token are
  * neither read nor written.  Ids outside [0, vocab) contribute nothing.
  * Errors: as tide_embedding; TIDE_ERR_INVALID also for a workspace too small or misaligned.
  */
