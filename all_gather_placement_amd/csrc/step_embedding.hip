@@ -486,25 +486,25 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(Embeddi
   }
 }
 
-// Few tokens: a workgroup for each, which looks at all ids, goes on if its own is the first of its row,
+// Few tokens (up to kMost): a workgroup for each, which looks at all ids, goes on if its own is the first of its row,
 // and sums the row's tokens, in ascending order or in ascending quarters.
-template <typename T, typename I, bool kWhole>
+template <typename T, typename I, bool kWhole, int kMost>
 __global__ __launch_bounds__(kThreads) void embedding_direct_kernel(EmbeddingBwdArgs a) {
-  constexpr int E = kVec<T>, kAhead = 16, kMasks = kDirectTokens / 64;
+  constexpr int E = kVec<T>, kAhead = 16, kMasks = kMost / 64;
   __shared__ uint64_t masks[kMasks];
-  __shared__ int list[kDirectTokens];
+  __shared__ int list[kMost];
   const I* __restrict__ ids = static_cast<const I*>(a.ids);
   const int tokens = int(a.tokens), lane = threadIdx.x & 63;
   const int64_t row = ids[blockIdx.x];
   if (uint64_t(row) >= uint64_t(a.vocab)) return;
-  I id[kDirectTokens / kThreads];
+  I id[kMost / kThreads];
 #pragma unroll
-  for (int j = 0; j < kDirectTokens / kThreads; ++j) {
+  for (int j = 0; j < kMost / kThreads; ++j) {
     const int t = j * kThreads + threadIdx.x;
     id[j] = t < tokens ? ids[t] : I(-1);
   }
 #pragma unroll
-  for (int j = 0; j < kDirectTokens / kThreads; ++j) {
+  for (int j = 0; j < kMost / kThreads; ++j) {
     const uint64_t same = __ballot(int64_t(id[j]) == row);
     if (lane == 0) masks[(j * kThreads + threadIdx.x) / 64] = same;
   }
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void embedding_direct_kernel(EmbeddingBwd
     if ((masks[k] & earlier) != 0) return;
   }
 #pragma unroll
-  for (int j = 0; j < kDirectTokens / kThreads; ++j) {
+  for (int j = 0; j < kMost / kThreads; ++j) {
     const int t = j * kThreads + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < kMasks; ++k)
@@ -583,16 +583,27 @@ __global__ __launch_bounds__(kThreads) void embedding_zero_kernel(T* table, int6
 // a launch of its own gain more: 500 MB 122 us instead of 127, 1 GB 202 instead of 214.
 constexpr int64_t kZeroBesideSort = int64_t(256) << 20;
 
+// Up to 1024 tokens are not sorted, 512 where rows are wide: 500 tokens of a text, 512 columns of bf16, 7 us
+// instead of 20, 4096 columns 45 instead of 55; 1000 tokens 10 instead of 22, 4096 columns 57 and 57.  One
+// workgroup sums all tokens of a row, so a long run of a wide row takes longer (500 of 4096 columns 105 us
+// instead of 25): tables of few such rows are left to the sort.
+inline bool sum_directly(int64_t tokens, int64_t vocab, int64_t vecs) {
+  if (vecs <= 64) return tokens <= 1024;
+  return tokens <= (vecs <= 256 ? 1024 : 512) && tokens <= 32 * vocab;
+}
+
 template <typename T, typename I, bool kWhole>
 void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
   const int64_t elems = a.accumulate ? 0 : a.vocab * a.dim;
-  const bool direct = a.tokens <= kDirectTokens, zero_first = direct || elems * int64_t(sizeof(T)) > kZeroBesideSort;
+  const bool direct = sum_directly(a.tokens, a.vocab, ceil_div(a.dim, kVec<T>)), zero_first = direct || elems * int64_t(sizeof(T)) > kZeroBesideSort;
   if (zero_first && elems > 0)
     hipLaunchKernelGGL((embedding_zero_kernel<T>), dim3(grid_of(elems, kThreads * kVec<T>)), dim3(kThreads), 0, s,
                        static_cast<T*>(a.dtable), elems);
   if (direct) {
-    if (a.tokens > 0)
-      hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
+    if (a.tokens > 512)
+      hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole, 1024>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
+    else if (a.tokens > 0)
+      hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole, 512>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
     return;
   }
   const int shift = sort_shift(a.vocab);

@@ -113,8 +113,6 @@ int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, int param_dtype,
 int launch_embedding(int64_t tokens, const void* ids, int ids_dtype, int64_t vocab, int64_t dim, const void* table,
                      int dtype, float scale, void* out, void* stream);
 
-// Up to so many tokens are not sorted.
-constexpr int kDirectTokens = 256;
 // The gradient's sort gives each of 2^shift workgroups the table rows v with v mod 2^shift its number;
 // it finds their tokens by reading all ids.  There is one for each compute unit at least, and none has
 // more than kSortMaxRows rows.

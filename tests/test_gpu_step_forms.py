@@ -208,6 +208,24 @@ def test_embedding_bwd_of_a_large_table(gpu_available, vocab, dim, dtype):
     within(embedding_bwd(ids, dy, vocab, 0.5, out=out), want, tol + uo(dtype) * (want.abs() + tol), "gradient")
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=str)
+@pytest.mark.parametrize("tokens", [511, 512, 513, 1023, 1024, 1025])
+@pytest.mark.parametrize("vocab,dim", [(3, 40), (5, 700), (90, 1001), (4000, 2100), (9000, 12)])
+def test_embedding_bwd_around_few_tokens(gpu_available, vocab, dim, tokens, dtype):
+    """With and without a sort: every token once, rows of none zero, in place and added."""
+    say("few tokens", tokens, vocab, dim, dtype)
+    ids = torch.randint(-1, vocab + 1, (tokens,), device="cuda", generator=gen(tokens))
+    ids[::4] = vocab // 2
+    dy = whole((tokens, dim), dtype, 3)
+    inside = (ids >= 0) & (ids < vocab)
+    want = torch.zeros((vocab, dim), dtype=torch.float64, device="cuda").index_add_(0, ids[inside], dy[inside].double())
+    out = torch.full((vocab, dim), float("nan"), dtype=dtype, device="cuda")
+    assert torch.equal(embedding_bwd(ids, dy, vocab, out=out), want.float().to(dtype))
+    old = whole((vocab, dim), dtype, 4)
+    got = embedding_bwd(ids.int(), dy, vocab, out=old.clone(), accumulate=True)
+    assert torch.equal(got, (want + old.double()).float().to(dtype))
+
+
 def test_embedding_bwd_does_not_depend_on_the_run(gpu_available):
     """The list of runs is made in any order; the sums are not."""
     ids = (torch.rand(40_000, device="cuda", generator=gen(1)).square().square() * 900).long()
