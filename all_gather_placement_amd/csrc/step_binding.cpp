@@ -179,19 +179,27 @@ PyObject* triple(const Output& a, const Output& b, const Output& c) {
 // Gradient norm and clipping
 // ---------------------------------------------------------------------------------------------
 
+// A reference to a Python object, which may be NULL.
+struct Held {
+  PyObject* o;
+  explicit Held(PyObject* owned) : o(owned) {}
+  Held(const Held& h) : o(h.o) { Py_XINCREF(o); }
+  Held& operator=(const Held&) = delete;
+  ~Held() { Py_XDECREF(o); }
+};
+
+// The tensors of a sequence or iterator.  They live as long as this does: what a generator makes would
+// otherwise be freed before the call is enqueued, and its memory given to the call's own workspace.
 struct List {
+  Held held;
   std::vector<void*> p;
   std::vector<int64_t> n;
   at::ScalarType type = at::kFloat;
   int32_t count() const { return int32_t(p.size()); }
 
-  List(const Device& d, PyObject* o, const char* name) {
-    PyObject* seq = PySequence_Fast(o, "a sequence of tensors is wanted");
+  List(const Device& d, PyObject* o, const char* name) : held(PySequence_Fast(o, "a sequence of tensors is wanted")) {
+    PyObject* seq = held.o;
     if (seq == nullptr) throw Refused();
-    struct Drop {
-      PyObject* o;
-      ~Drop() { Py_DECREF(o); }
-    } drop{seq};
     const Py_ssize_t size = PySequence_Fast_GET_SIZE(seq);
     NEED(size <= INT32_MAX, "too many ", name);
     p.reserve(size_t(size));
@@ -210,7 +218,7 @@ struct List {
 };
 
 // outs: like the gradients, or None for the gradients themselves.
-List outputs(const Device& d, PyObject* o, PyObject* grads, const List& g) {
+List outputs(const Device& d, PyObject* o, const List& g) {
   if (o == Py_None) return g;
   List outs(d, o, "outs");
   NEED(outs.n == g.n, "outs must have the gradients' sizes");
@@ -263,14 +271,15 @@ PyObject* grad_clip(Args a, Py_ssize_t n) {
   arity(n, 5);
   const at::Tensor& sumsq = tensor(a[1], "sumsq");
   on_gpu(sumsq, "sumsq");
+  const double max_norm = number(a[2]);  // before addresses are taken: it may run Python code
   const Device d;
   const List g(d, a[0], "grads");
-  const List outs = outputs(d, a[3], a[0], g);
+  const List outs = outputs(d, a[3], g);
   const Output norm(a[4], "norm", [&] { return d.empty({}, at::kFloat); });
   one_value(d, norm.t, "norm", at::kFloat);
   one_value(d, &sumsq, "sumsq", at::kDouble);
   check(tide_grad_clip(g.count(), g.p.data(), outs.p.data(), g.n.data(), code(g.type),
-                       static_cast<double*>(sumsq.data_ptr()), number(a[2]), static_cast<float*>(at_of(norm.t)),
+                       static_cast<double*>(sumsq.data_ptr()), max_norm, static_cast<float*>(at_of(norm.t)),
                        d.stream()),
         "tide_grad_clip");
   return norm.result();
@@ -280,9 +289,10 @@ PyObject* grad_clip(Args a, Py_ssize_t n) {
 PyObject* clip_grad_norm(Args a, Py_ssize_t n) {
   arity(n, 6);
   first_on_gpu(a[0], "grads");
+  const double max_norm = number(a[1]);  // as in grad_clip
   const Device d;
   const List g(d, a[0], "grads");
-  const List outs = outputs(d, a[2], a[0], g);
+  const List outs = outputs(d, a[2], g);
   const Output norm(a[3], "norm", [&] { return d.empty({}, at::kFloat); });
   const Opt sumsq = optional(a[4], "sumsq");
   one_value(d, norm.t, "norm", at::kFloat);
@@ -290,7 +300,7 @@ PyObject* clip_grad_norm(Args a, Py_ssize_t n) {
   const int type = code(g.type);
   const Workspace ws(d, optional(a[5], "workspace"), tide_grad_norm_workspace(g.count(), g.n.data(), type),
                      "tide_clip_grad_norm");
-  check(tide_clip_grad_norm(g.count(), g.p.data(), outs.p.data(), g.n.data(), type, number(a[1]),
+  check(tide_clip_grad_norm(g.count(), g.p.data(), outs.p.data(), g.n.data(), type, max_norm,
                             static_cast<double*>(at_of(sumsq)), static_cast<float*>(at_of(norm.t)), ws.p, ws.bytes,
                             d.stream()),
         "tide_clip_grad_norm");

@@ -1,0 +1,89 @@
+"""Calls of the training-step operators as a program makes them: lists that live only as long as the call."""
+import weakref
+
+import pytest
+import torch
+
+from all_gather_placement_amd import TideError, clip_grad_norm, grad_clip, grad_norm, load_step_binding
+from test_gpu_step import BF16, FP32, normal, say
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------
+# Sequences of tensors
+# ------------------------------------------------------------------------------------------------
+
+class Sequence:
+    """A sequence that makes its tensors when it is asked for them."""
+
+    def __init__(self, make, n):
+        self.make, self.n = make, n
+
+    def __len__(self):
+        return self.n
+
+    def __getitem__(self, i):
+        if i >= self.n:
+            raise IndexError(i)
+        return self.make(i)
+
+
+@pytest.mark.parametrize("kind", ["generator", "sequence", "map"])
+@pytest.mark.parametrize("call", ["grad_norm", "clip_grad_norm", "grad_clip"])
+def test_made_tensors_live_until_the_call_is_enqueued(gpu_available, call, kind):
+    """The stream is asked for last, when everything has been allocated and before a kernel is launched.
+    It is refused here, so the call ends without one."""
+    say("made tensors", call, kind)
+    made = []
+
+    def make(i):
+        t = torch.zeros(5000, device="cuda")
+        made.append(weakref.ref(t))
+        return t
+
+    def tensors():
+        return {"generator": lambda: (make(i) for i in range(3)), "sequence": lambda: Sequence(make, 3),
+                "map": lambda: map(make, range(3))}[kind]()
+
+    alive = []
+
+    def stream_of(device):
+        alive.append([r() is not None for r in made[-n:]])
+        raise KeyError("no stream")
+
+    sumsq = torch.ones((), dtype=torch.float64, device="cuda")
+    kept = [torch.zeros(5000, device="cuda") for _ in range(3)]
+    binding = load_step_binding()
+    binding.configure(TideError, stream_of)
+    try:
+        for args, n in ((dict(grads=tensors), 3), (dict(grads=lambda: kept, outs=tensors), 3),
+                        (dict(grads=tensors, outs=tensors), 6)):
+            if call == "grad_norm" and "outs" in args:
+                continue
+            args = {k: f() for k, f in args.items()}
+            with pytest.raises(KeyError):
+                if call == "grad_norm":
+                    grad_norm(args["grads"])
+                elif call == "clip_grad_norm":
+                    clip_grad_norm(args["grads"], 1.0, outs=args.get("outs"))
+                else:
+                    grad_clip(args["grads"], sumsq, 1.0, outs=args.get("outs"))
+            assert alive.pop() == [True] * n
+    finally:
+        binding.configure(TideError, torch._C._cuda_getCurrentRawStream)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=str)
+def test_generators_give_what_lists_give(gpu_available, dtype):
+    say("generators", dtype)
+    grads = [normal((20_000 + 4097 * i,), dtype, i) for i in range(40)]
+    want = grad_norm([g * 0.5 for g in grads])
+    outs = [torch.empty_like(g) for g in grads]
+    clip_grad_norm([g * 0.5 for g in grads], 1.0, outs=outs)
+    for _ in range(3):
+        assert torch.equal(grad_norm(g * 0.5 for g in grads), want)
+        got = [torch.empty_like(g) for g in grads]
+        assert torch.equal(clip_grad_norm((g * 0.5 for g in grads), 1.0, outs=(o for o in got)), want)
+        assert all(map(torch.equal, got, outs))
+    assert torch.equal(grad_norm(tuple(g * 0.5 for g in grads)), want)
