@@ -173,22 +173,24 @@ __device__ __forceinline__ uint64_t same_row(int row, uint64_t active, int bits,
   return same;
 }
 
-// Workgroups below `ranges` sort; the others, if any, write zeros to the table, one 16-byte store a
-// thread: short-lived workgroups in order of address write fastest (131072 x 4096 bf16 with 256 threads
-// 157 us, 1024 threads 169, a wave for each row 194).  Rows that have tokens are written again by the
-// sums, which costs less than asking for each row whether it has any (237 us with the sums, 30 more).
+// Workgroups below `sorting` sort, the ranges from `first_range` on; the others, if any, write zeros to the
+// table, one 16-byte store a thread: short-lived workgroups in order of address write fastest (131072 x 4096
+// bf16 with 256 threads 157 us, 1024 threads 169, a wave for each row 194).  Rows that have tokens are written
+// again by the sums, which costs less than asking for each row whether it has any (237 us with the sums, 30
+// more).
 //
 // 50021 tokens of a text over 20011 rows: 20 us; with the ids read once more for the places 24, without
 // a queue or list, a few tokens at a time, 28, and with a row's lanes found by all of its bits 44.
 template <typename T, typename I>
-__global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingBwdArgs a, unsigned ranges, int shift,
+__global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingBwdArgs a, unsigned first_range,
+                                                                      unsigned sorting, unsigned ranges, int shift,
                                                                       int most_rows, int bits) {
-  if (blockIdx.x >= ranges) {
+  if (blockIdx.x >= sorting) {
     constexpr int N = kVec<T>;
     const float none[N] = {};
     const int64_t end = a.vocab * a.dim;
-    for (int64_t e = (int64_t(blockIdx.x - ranges) * kSortThreads + threadIdx.x) * N; e < end;
-         e += int64_t(gridDim.x - ranges) * kSortThreads * N)
+    for (int64_t e = (int64_t(blockIdx.x - sorting) * kSortThreads + threadIdx.x) * N; e < end;
+         e += int64_t(gridDim.x - sorting) * kSortThreads * N)
       store_vec<T, N, false, false>(static_cast<T*>(a.dtable) + e, tail<N>(end - e), none);
     return;
   }
@@ -196,7 +198,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(EmbeddingB
   __shared__ int lds[kSortWaves];
   __shared__ alignas(16) unsigned lists[kSortWaves][kListed];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const unsigned vocab = unsigned(a.vocab), range = blockIdx.x, mask = (1u << shift) - 1;
+  const unsigned vocab = unsigned(a.vocab), range = first_range + blockIdx.x, mask = (1u << shift) - 1;
   const int rows = int((vocab - range + mask) >> shift);  // range, range + 2^shift, ...: at least one
   for (int i = threadIdx.x; i < kSortWaves * most_rows; i += kSortThreads) count[i] = 0;
 
@@ -607,13 +609,17 @@ void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
     return;
   }
   const int shift = sort_shift(a.vocab);
-  const int64_t ranges = int64_t(1) << shift, rows = ceil_div(a.vocab, ranges);
+  const int64_t owners = int64_t(1) << shift, rows = ceil_div(a.vocab, owners);
   int bits = 0;
   while ((1 << bits) < rows) ++bits;
-  const unsigned sorting = unsigned(a.vocab < ranges ? a.vocab : ranges);
-  const unsigned zeroing = zero_first || elems == 0 ? 0 : grid_of(elems, kSortThreads * kVec<T>);
-  hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(sorting + zeroing), dim3(kSortThreads),
-                     kSortWaves * rows * sizeof(int), s, a, sorting, shift, int(rows), bits);
+  const unsigned ranges = unsigned(a.vocab < owners ? a.vocab : owners);
+  unsigned zeroing = zero_first || elems == 0 ? 0 : grid_of(elems, kSortThreads * kVec<T>);
+  // workgroups do not go on to another range: tables of more than 2^30 rows take a second launch
+  for (unsigned first = 0; first < ranges; first += unsigned(kMaxGrid), zeroing = 0) {
+    const unsigned sorting = ranges - first < kMaxGrid ? ranges - first : unsigned(kMaxGrid);
+    hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(sorting + zeroing), dim3(kSortThreads),
+                       kSortWaves * rows * sizeof(int), s, a, first, sorting, ranges, shift, int(rows), bits);
+  }
   const int64_t pieces = ceil_div(a.tokens, kPiece), chunks = ceil_div(ceil_div(a.dim, kVec<T>), 64);
   hipLaunchKernelGGL((embedding_sum_kernel<T, kWhole>), dim3(grid_of(pieces * chunks, 4)), dim3(kThreads), 0, s, a);
   // how many runs there are is known on the device only

@@ -1,11 +1,12 @@
-"""Calls of the training-step operators as a program makes them: lists that live only as long as the call."""
+"""Calls of the training-step operators as a program makes them: lists that live only as long as the call,
+sizes beyond one launch."""
 import weakref
 
 import pytest
 import torch
 
-from all_gather_placement_amd import TideError, clip_grad_norm, grad_clip, grad_norm, load_step_binding
-from test_gpu_step import BF16, FP32, normal, say
+from all_gather_placement_amd import TideError, clip_grad_norm, embedding_bwd, grad_clip, grad_norm, load_step_binding
+from test_gpu_step import BF16, FP32, gen, normal, say, whole
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,30 @@ def test_generators_give_what_lists_give(gpu_available, dtype):
         assert torch.equal(clip_grad_norm((g * 0.5 for g in grads), 1.0, outs=(o for o in got)), want)
         assert all(map(torch.equal, got, outs))
     assert torch.equal(grad_norm(tuple(g * 0.5 for g in grads)), want)
+
+
+# ------------------------------------------------------------------------------------------------
+# Sizes beyond one launch
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("vocab", [(1 << 30) - 1, (1 << 30) + 3, (1 << 31) - 1])
+def test_table_gradient_of_more_rows_than_one_launch_sorts(gpu_available, vocab):
+    say("table of many rows", vocab)
+    tokens = 1100  # above what is summed without a sort
+    ids = torch.randint(0, vocab, (tokens,), device="cuda", generator=gen(1))
+    ids[:6] = torch.tensor([0, vocab - 1, vocab // 2, vocab - 2, 1 << 29, (1 << 22) - 1], device="cuda")
+    ids[100:200] = vocab - 1
+    ids[200:300] = 7
+    ids[300] = vocab
+    dy = whole((tokens, 1), BF16, 2, 1, 5)
+    rows, places = ids.unique(return_inverse=True)
+    want = torch.zeros((rows.numel(), 1), dtype=torch.float64, device="cuda").index_add_(0, places, dy.double())
+    keep = rows < vocab
+    rows, want = rows[keep], want[keep]
+    grad = embedding_bwd(ids, dy, vocab)
+    # sums of whole numbers: exact in fp32, rounded once
+    assert torch.equal(grad[rows], want.float().bfloat16())
+    assert int(torch.count_nonzero(grad)) == rows.numel()
+    embedding_bwd(ids, dy, vocab, out=grad, accumulate=True)
+    assert torch.equal(grad[rows], (want + want.float().bfloat16().double()).float().bfloat16())
+    assert int(torch.count_nonzero(grad)) == rows.numel()
