@@ -195,9 +195,23 @@ __device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[E]) {
 }
 // f(whole) as a constant: rows of `cols` elements are of whole vectors of E, or not.
 template <int E, typename F>
-void with_whole(int64_t cols, F&& f) {
-  if (cols % E == 0) f(std::true_type());
-  else f(std::false_type());
+int with_whole(int64_t cols, F&& f) {
+  return cols % E == 0 ? f(std::true_type()) : f(std::false_type());
+}
+// Launches a kernel and returns its own status (a hipError_t): what an earlier call of another library left
+// behind is neither reported nor cleared.  A call ends at its first failed launch, since later kernels read
+// what earlier ones write.
+template <typename T>
+struct Same {
+  typedef T type;
+};
+template <typename... P>
+int launch(void (*kernel)(P...), dim3 grid, int threads, size_t lds, hipStream_t s,
+           const typename Same<P>::type&... args) {
+  void* p[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), p, lds, s);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
 }
 // Elements of a 16-byte vector.
 template <typename T>

@@ -595,18 +595,20 @@ inline bool sum_directly(int64_t tokens, int64_t vocab, int64_t vecs) {
 }
 
 template <typename T, typename I, bool kWhole>
-void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
+int gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
   const int64_t elems = a.accumulate ? 0 : a.vocab * a.dim;
-  const bool direct = sum_directly(a.tokens, a.vocab, ceil_div(a.dim, kVec<T>)), zero_first = direct || elems * int64_t(sizeof(T)) > kZeroBesideSort;
+  const bool direct = sum_directly(a.tokens, a.vocab, ceil_div(a.dim, kVec<T>));
+  const bool zero_first = direct || elems * int64_t(sizeof(T)) > kZeroBesideSort;
+  int e = 0;
   if (zero_first && elems > 0)
-    hipLaunchKernelGGL((embedding_zero_kernel<T>), dim3(grid_of(elems, kThreads * kVec<T>)), dim3(kThreads), 0, s,
-                       static_cast<T*>(a.dtable), elems);
+    e = launch(embedding_zero_kernel<T>, grid_of(elems, kThreads * kVec<T>), kThreads, 0, s, static_cast<T*>(a.dtable),
+               elems);
+  if (e != 0) return e;
   if (direct) {
     if (a.tokens > 512)
-      hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole, 1024>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
-    else if (a.tokens > 0)
-      hipLaunchKernelGGL((embedding_direct_kernel<T, I, kWhole, 512>), dim3(unsigned(a.tokens)), dim3(kThreads), 0, s, a);
-    return;
+      return launch(embedding_direct_kernel<T, I, kWhole, 1024>, unsigned(a.tokens), kThreads, 0, s, a);
+    if (a.tokens > 0) return launch(embedding_direct_kernel<T, I, kWhole, 512>, unsigned(a.tokens), kThreads, 0, s, a);
+    return e;
   }
   const int shift = sort_shift(a.vocab);
   const int64_t owners = int64_t(1) << shift, rows = ceil_div(a.vocab, owners);
@@ -615,21 +617,22 @@ void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
   const unsigned ranges = unsigned(a.vocab < owners ? a.vocab : owners);
   unsigned zeroing = zero_first || elems == 0 ? 0 : grid_of(elems, kSortThreads * kVec<T>);
   // workgroups do not go on to another range: tables of more than 2^30 rows take a second launch
-  for (unsigned first = 0; first < ranges; first += unsigned(kMaxGrid), zeroing = 0) {
+  for (unsigned first = 0; first < ranges && e == 0; first += unsigned(kMaxGrid), zeroing = 0) {
     const unsigned sorting = ranges - first < kMaxGrid ? ranges - first : unsigned(kMaxGrid);
-    hipLaunchKernelGGL((embedding_sort_kernel<T, I>), dim3(sorting + zeroing), dim3(kSortThreads),
-                       kSortWaves * rows * sizeof(int), s, a, first, sorting, ranges, shift, int(rows), bits);
+    e = launch(embedding_sort_kernel<T, I>, sorting + zeroing, kSortThreads, kSortWaves * rows * sizeof(int), s, a, first,
+               sorting, ranges, shift, int(rows), bits);
   }
+  if (e != 0) return e;
   const int64_t pieces = ceil_div(a.tokens, kPiece), chunks = ceil_div(ceil_div(a.dim, kVec<T>), 64);
-  hipLaunchKernelGGL((embedding_sum_kernel<T, kWhole>), dim3(grid_of(pieces * chunks, 4)), dim3(kThreads), 0, s, a);
+  e = launch(embedding_sum_kernel<T, kWhole>, grid_of(pieces * chunks, 4), kThreads, 0, s, a);
+  if (e != 0) return e;
   // how many runs there are is known on the device only
-  hipLaunchKernelGGL((embedding_join_kernel<T, kWhole>),
-                     dim3(kJoinLongWgs + kJoinShortWgs, unsigned(chunks < 64 ? chunks : 64)), dim3(kJoinWaves * 64), 0,
-                     s, a);
+  return launch(embedding_join_kernel<T, kWhole>,
+                dim3(kJoinLongWgs + kJoinShortWgs, unsigned(chunks < 64 ? chunks : 64)), kJoinWaves * 64, 0, s, a);
 }
 template <typename T, typename I>
-void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
-  with_whole<kVec<T>>(a.dim, [&](auto w) { gradient<T, I, decltype(w)::value>(a, s); });
+int gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
+  return with_whole<kVec<T>>(a.dim, [&](auto w) { return gradient<T, I, decltype(w)::value>(a, s); });
 }
 
 // Two vectors a lane and up to four waves a row: 65536 rows of 4096 bf16 (20132 distinct of 131072) in
@@ -637,26 +640,25 @@ void gradient(const EmbeddingBwdArgs& a, hipStream_t s) {
 // output is written past the caches, which keep the table's frequent rows: with plain stores 142 us, and
 // 18 us against 19 at 8192 rows, where it would fit.
 template <typename T, typename I>
-void lookup(int64_t tokens, const void* ids, int64_t vocab, int64_t dim, const void* table, float scale, void* out,
+int lookup(int64_t tokens, const void* ids, int64_t vocab, int64_t dim, const void* table, float scale, void* out,
             hipStream_t s) {
   constexpr int NV = 2, NT = 4;
   const int64_t vecs = ceil_div(dim, kVec<T>);
   const auto* i = static_cast<const I*>(ids);
   const auto* w = static_cast<const T*>(table);
   auto* o = static_cast<T*>(out);
-  with_whole<kVec<T>>(dim, [&](auto wh) {
+  return with_whole<kVec<T>>(dim, [&](auto wh) {
     constexpr bool whole = decltype(wh)::value;
     if (vecs < 64) {
       int lshift = 0;
       while ((1 << lshift) < vecs) ++lshift;
       const int64_t per = int64_t(kThreads >> lshift) * NT;
-      hipLaunchKernelGGL((embedding_narrow_kernel<T, I, NT, whole>), dim3(grid_of(tokens, per)), dim3(kThreads), 0, s,
-                         tokens, i, vocab, int(dim), w, scale, o, lshift);
-      return;
+      return launch(embedding_narrow_kernel<T, I, NT, whole>, grid_of(tokens, per), kThreads, 0, s, tokens, i, vocab,
+                    int(dim), w, scale, o, lshift);
     }
     const int wshift = vecs <= 64 * NV ? 0 : vecs <= 128 * NV ? 1 : 2;
-    hipLaunchKernelGGL((embedding_rows_kernel<T, I, NV, whole>), dim3(grid_of(tokens, 4 >> wshift)), dim3(kThreads), 0,
-                       s, tokens, i, vocab, dim, w, scale, o, wshift);
+    return launch(embedding_rows_kernel<T, I, NV, whole>, grid_of(tokens, 4 >> wshift), kThreads, 0, s, tokens, i, vocab,
+                  dim, w, scale, o, wshift);
   });
 }
 
@@ -665,26 +667,16 @@ void lookup(int64_t tokens, const void* ids, int64_t vocab, int64_t dim, const v
 int launch_embedding(int64_t tokens, const void* ids, int ids_dtype, int64_t vocab, int64_t dim, const void* table,
                      int dtype, float scale, void* out, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dtype == TIDE_BF16) {
-    if (ids_dtype == TIDE_INT32) lookup<bf16_t, int32_t>(tokens, ids, vocab, dim, table, scale, out, s);
-    else lookup<bf16_t, int64_t>(tokens, ids, vocab, dim, table, scale, out, s);
-  } else {
-    if (ids_dtype == TIDE_INT32) lookup<float, int32_t>(tokens, ids, vocab, dim, table, scale, out, s);
-    else lookup<float, int64_t>(tokens, ids, vocab, dim, table, scale, out, s);
-  }
-  return hipGetLastError();
+  const auto call = [&](auto f) { return f(tokens, ids, vocab, dim, table, scale, out, s); };
+  if (dtype == TIDE_BF16) return call(ids_dtype == TIDE_INT32 ? lookup<bf16_t, int32_t> : lookup<bf16_t, int64_t>);
+  return call(ids_dtype == TIDE_INT32 ? lookup<float, int32_t> : lookup<float, int64_t>);
 }
 
 int launch_embedding_bwd(const EmbeddingBwdArgs& a, int dtype, int ids_dtype, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dtype == TIDE_BF16) {
-    if (ids_dtype == TIDE_INT32) gradient<bf16_t, int32_t>(a, s);
-    else gradient<bf16_t, int64_t>(a, s);
-  } else {
-    if (ids_dtype == TIDE_INT32) gradient<float, int32_t>(a, s);
-    else gradient<float, int64_t>(a, s);
-  }
-  return hipGetLastError();
+  if (dtype == TIDE_BF16)
+    return ids_dtype == TIDE_INT32 ? gradient<bf16_t, int32_t>(a, s) : gradient<bf16_t, int64_t>(a, s);
+  return ids_dtype == TIDE_INT32 ? gradient<float, int32_t>(a, s) : gradient<float, int64_t>(a, s);
 }
 
 }  // namespace tide_step

@@ -647,10 +647,9 @@ bool with_bwd_rows(int64_t vecs, F&& f) {
 // fit lose up to 10% that way (8192 x 4096 forward: 26 instead of 24).
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
 template <int E, typename F>
-void with_form(int64_t bytes, int64_t cols, F&& f) {
-  with_whole<E>(cols, [&](auto whole) {
-    if (bytes > kCacheBytes) f(std::true_type(), whole);
-    else f(std::false_type(), whole);
+int with_form(int64_t bytes, int64_t cols, F&& f) {
+  return with_whole<E>(cols, [&](auto whole) {
+    return bytes > kCacheBytes ? f(std::true_type(), whole) : f(std::false_type(), whole);
   });
 }
 
@@ -659,82 +658,74 @@ void with_form(int64_t bytes, int64_t cols, F&& f) {
 constexpr int kFewRows = 16;
 
 template <typename T, typename PT>
-void forward(const LayerNormArgs& a, hipStream_t s) {
+int forward(const LayerNormArgs& a, hipStream_t s) {
   const int64_t vecs = ceil_div(a.cols, kVec<T>);
-  with_form<kVec<T>>(2 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {
+  return with_form<kVec<T>>(2 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {
     constexpr bool once = decltype(o)::value, whole = decltype(w)::value;
+    int e = 0;
     if (vecs <= 64) {
       with_lanes(vecs, [&](auto l) {
         constexpr int L = decltype(l)::value;
         const int64_t grid = min64(ceil_div(a.rows, kNarrowThreads / L), kMaxGrid);
-        hipLaunchKernelGGL((layer_norm_narrow_kernel<T, PT, L, once, whole>), dim3(unsigned(grid)), dim3(kNarrowThreads), 0, s,
-                           a);
+        e = launch(layer_norm_narrow_kernel<T, PT, L, once, whole>, unsigned(grid), kNarrowThreads, 0, s, a);
       });
-      return;
+      return e;
     }
     const bool fits = with_rows(vecs, a.rows, [&](auto nv, auto rb, int waves) {
       constexpr int NV = decltype(nv)::value, RB = decltype(rb)::value;
       const int64_t grid = min64(ceil_div(a.rows, RB), kMaxGrid);
-      hipLaunchKernelGGL((layer_norm_rows_kernel<T, PT, NV, RB, once, whole>), dim3(unsigned(grid)), dim3(waves * 64), 0, s, a);
+      e = launch(layer_norm_rows_kernel<T, PT, NV, RB, once, whole>, unsigned(grid), waves * 64, 0, s, a);
     });
-    if (!fits)
-      hipLaunchKernelGGL((layer_norm_wide_kernel<T, PT>), dim3(unsigned(min64(a.rows, kMaxGrid))), dim3(kWideThreads),
-                         0, s, a);
+    if (fits) return e;
+    return launch(layer_norm_wide_kernel<T, PT>, unsigned(min64(a.rows, kMaxGrid)), kWideThreads, 0, s, a);
   });
 }
 
 template <typename T, typename PT>
-void backward(LayerNormBwdArgs a, int groups, hipStream_t s) {
+int backward(LayerNormBwdArgs a, int groups, hipStream_t s) {
   const bool params = a.dweight != nullptr || a.dbias != nullptr;
   const int64_t vecs = ceil_div(a.cols, kVec<T>);
-  if (params && a.rows > 0 && a.rows <= kFewRows && vecs <= 64 * kMaxWaves * 2) {
-    with_whole<kVec<T>>(a.cols, [&](auto w) {
+  if (params && a.rows > 0 && a.rows <= kFewRows && vecs <= 64 * kMaxWaves * 2)
+    return with_whole<kVec<T>>(a.cols, [&](auto w) {
       constexpr bool whole = decltype(w)::value;
       const unsigned rows = a.dx != nullptr ? unsigned(a.rows) : 0, cols = unsigned(ceil_div(vecs, 64));
-      const auto launch = [&](unsigned row_wgs, unsigned col_wgs) {
+      const auto few = [&](unsigned row_wgs, unsigned col_wgs) {
         if (vecs <= 64 * kMaxWaves)
-          hipLaunchKernelGGL((layer_norm_bwd_few_kernel<T, PT, 1, whole>), dim3(row_wgs + col_wgs), dim3(cols * 64), 0, s,
-                             a, row_wgs);
-        else
-          hipLaunchKernelGGL((layer_norm_bwd_few_kernel<T, PT, 2, whole>), dim3(row_wgs + col_wgs),
-                             dim3(ceil_div(vecs, 128) * 64), 0, s, a, row_wgs);
+          return launch(layer_norm_bwd_few_kernel<T, PT, 1, whole>, row_wgs + col_wgs, int(cols) * 64, 0, s, a, row_wgs);
+        return launch(layer_norm_bwd_few_kernel<T, PT, 2, whole>, row_wgs + col_wgs, int(ceil_div(vecs, 128)) * 64, 0,
+                      s, a, row_wgs);
       };
-      if (a.dx == a.dy) {  // the sums first: they read dy too
-        launch(0, cols);
-        launch(rows, 0);
-      } else {
-        launch(rows, cols);
-      }
+      if (a.dx != a.dy) return few(rows, cols);
+      const int e = few(0, cols);  // the sums first: they read dy too
+      return e != 0 ? e : few(rows, 0);
     });
-    return;
-  }
   if (!params) a.partial = nullptr;
+  int e = 0;
   if (a.rows > 0)
-    with_form<kVec<T>>(3 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {
+    e = with_form<kVec<T>>(3 * a.rows * a.cols * int64_t(sizeof(T)), a.cols, [&](auto o, auto w) {
       constexpr bool once = decltype(o)::value, whole = decltype(w)::value;
+      int e = 0;
       if (vecs <= 64) {
         with_lanes(vecs, [&](auto l) {
-          hipLaunchKernelGGL((layer_norm_bwd_narrow_kernel<T, PT, decltype(l)::value, once, whole>), dim3(unsigned(groups)),
-                             dim3(kNarrowThreads), 0, s, a);
+          e = launch(layer_norm_bwd_narrow_kernel<T, PT, decltype(l)::value, once, whole>, unsigned(groups),
+                     kNarrowThreads, 0, s, a);
         });
-        return;
+        return e;
       }
       const bool fits = with_bwd_rows(vecs, [&](auto nv, auto rb, int waves) {
-        hipLaunchKernelGGL((layer_norm_bwd_rows_kernel<T, PT, decltype(nv)::value, decltype(rb)::value, once, whole>),
-                           dim3(unsigned(groups)), dim3(waves * 64), 0, s, a);
+        e = launch(layer_norm_bwd_rows_kernel<T, PT, decltype(nv)::value, decltype(rb)::value, once, whole>,
+                   unsigned(groups), waves * 64, 0, s, a);
       });
-      if (fits) return;
+      if (fits) return e;
       // the sums first: dx may lie where dy does
       if (params)
-        hipLaunchKernelGGL((layer_norm_bwd_cols_kernel<T>), dim3(unsigned(ceil_div(vecs, 64)), unsigned(groups)),
-                           dim3(64), 0, s, a);
-      if (a.dx != nullptr)
-        hipLaunchKernelGGL((layer_norm_bwd_wide_kernel<T, PT>), dim3(unsigned(min64(a.rows, kMaxGrid))),
-                           dim3(kWideThreads), 0, s, a);
+        e = launch(layer_norm_bwd_cols_kernel<T>, dim3(unsigned(ceil_div(vecs, 64)), unsigned(groups)), 64, 0, s, a);
+      if (e != 0 || a.dx == nullptr) return e;
+      return launch(layer_norm_bwd_wide_kernel<T, PT>, unsigned(min64(a.rows, kMaxGrid)), kWideThreads, 0, s, a);
     });
-  if (params)
-    hipLaunchKernelGGL((layer_norm_join_kernel<PT>), dim3(unsigned(ceil_div(2 * padded(a.cols), 64))), dim3(256), 0, s,
-                       a.partial, groups, a.cols, static_cast<PT*>(a.dweight), static_cast<PT*>(a.dbias));
+  if (e != 0 || !params) return e;
+  return launch(layer_norm_join_kernel<PT>, unsigned(ceil_div(2 * padded(a.cols), 64)), 256, 0, s, a.partial, groups,
+                a.cols, static_cast<PT*>(a.dweight), static_cast<PT*>(a.dbias));
 }
 
 // Workgroups: as many as are resident at 16 waves a compute unit, each with at least two turns.
@@ -758,27 +749,16 @@ int layer_norm_bwd_groups(int64_t rows, int64_t cols, int dtype) {
 
 int launch_layer_norm(const LayerNormArgs& a, int dtype, int param_dtype, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dtype == TIDE_BF16) {
-    if (param_dtype == TIDE_BF16) forward<bf16_t, bf16_t>(a, s);
-    else forward<bf16_t, float>(a, s);
-  } else {
-    if (param_dtype == TIDE_BF16) forward<float, bf16_t>(a, s);
-    else forward<float, float>(a, s);
-  }
-  return hipGetLastError();
+  if (dtype == TIDE_BF16) return param_dtype == TIDE_BF16 ? forward<bf16_t, bf16_t>(a, s) : forward<bf16_t, float>(a, s);
+  return param_dtype == TIDE_BF16 ? forward<float, bf16_t>(a, s) : forward<float, float>(a, s);
 }
 
 int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, int param_dtype, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int groups = layer_norm_bwd_groups(a.rows, a.cols, dtype);
-  if (dtype == TIDE_BF16) {
-    if (param_dtype == TIDE_BF16) backward<bf16_t, bf16_t>(a, groups, s);
-    else backward<bf16_t, float>(a, groups, s);
-  } else {
-    if (param_dtype == TIDE_BF16) backward<float, bf16_t>(a, groups, s);
-    else backward<float, float>(a, groups, s);
-  }
-  return hipGetLastError();
+  if (dtype == TIDE_BF16)
+    return param_dtype == TIDE_BF16 ? backward<bf16_t, bf16_t>(a, groups, s) : backward<bf16_t, float>(a, groups, s);
+  return param_dtype == TIDE_BF16 ? backward<float, bf16_t>(a, groups, s) : backward<float, float>(a, groups, s);
 }
 
 }  // namespace tide_step

@@ -240,11 +240,8 @@ __global__ __launch_bounds__(kOneWgThreads) void clip_one_kernel(ClipTable t, do
 
 template <typename T>
 static int norm_partial(const NormTable& t, double* partial, int grid, hipStream_t s) {
-  if (t.sumsq != nullptr || t.norm != nullptr)
-    hipLaunchKernelGGL(norm_one_kernel<T>, dim3(1), dim3(kOneWgThreads), 0, s, t);
-  else
-    hipLaunchKernelGGL(norm_partial_kernel<T>, dim3(grid), dim3(kNormThreads), 0, s, t, partial);
-  return hipGetLastError();
+  if (t.sumsq != nullptr || t.norm != nullptr) return launch(norm_one_kernel<T>, 1, kOneWgThreads, 0, s, t);
+  return launch(norm_partial_kernel<T>, grid, kNormThreads, 0, s, t, partial);
 }
 int launch_norm_partial(const NormTable& t, int dtype, double* partial, int grid, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -253,20 +250,14 @@ int launch_norm_partial(const NormTable& t, int dtype, double* partial, int grid
 
 int launch_norm_finish(const double* partial, int n, double* sumsq, float* norm, void* stream) {
   if (sumsq == nullptr && norm == nullptr) return hipSuccess;
-  hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(kOneWgThreads), 0, static_cast<hipStream_t>(stream), partial, n,
-                     sumsq, norm);
-  return hipGetLastError();
+  return launch(norm_finish_kernel, 1, kOneWgThreads, 0, static_cast<hipStream_t>(stream), partial, n, sumsq, norm);
 }
 
 template <typename T>
 static int clip(const ClipTable& t, const double* sumsq, double max_norm, float* norm, int grid, hipStream_t s) {
-  if (t.partial != nullptr)
-    hipLaunchKernelGGL(clip_adding_kernel<T>, dim3(grid), dim3(kNormThreads), 0, s, t, max_norm, norm);
-  else if (t.sum_to != nullptr)
-    hipLaunchKernelGGL(clip_one_kernel<T>, dim3(1), dim3(kOneWgThreads), 0, s, t, max_norm, norm);
-  else
-    hipLaunchKernelGGL(clip_kernel<T>, dim3(grid * kClipParts), dim3(kNormThreads), 0, s, t, sumsq, max_norm, norm);
-  return hipGetLastError();
+  if (t.partial != nullptr) return launch(clip_adding_kernel<T>, grid, kNormThreads, 0, s, t, max_norm, norm);
+  if (t.sum_to != nullptr) return launch(clip_one_kernel<T>, 1, kOneWgThreads, 0, s, t, max_norm, norm);
+  return launch(clip_kernel<T>, grid * kClipParts, kNormThreads, 0, s, t, sumsq, max_norm, norm);
 }
 int launch_clip(const ClipTable& t, int dtype, const double* sumsq, double max_norm, float* norm, int grid,
                 void* stream) {

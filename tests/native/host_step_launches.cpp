@@ -2,12 +2,14 @@
 // refuses what the runtime refuses, and looks at what each call launches.  Exit status 0 = all checks passed.
 //
 //   host_step_launches sort     table gradients up to the largest vocabulary that is accepted
+//   host_step_launches failed   no kernel follows one that was not launched
+//   host_step_launches stale    an error of another library's earlier call is neither reported nor cleared
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
-#include <cstring>
+#include <functional>
 #include <map>
 #include <string>
 #include <vector>
@@ -38,6 +40,7 @@ struct Launch {
 static std::vector<Launch> launches;
 static void (*on_launch)(const Launch&, void** args) = nullptr;
 static hipError_t last_error = hipSuccess;
+static size_t fail_at = SIZE_MAX;  // the launch of a call that is refused
 
 static std::map<const void*, std::string>& names() {  // the library registers before this file's statics exist
   static std::map<const void*, std::string> m;
@@ -75,7 +78,7 @@ hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, si
   // less than 2^32 threads along an axis, up to 1024 in a workgroup, 64 KiB of its memory
   const auto axis = [](unsigned g, unsigned b) { return g > 0 && b > 0 && uint64_t(g) * b < (uint64_t(1) << 32); };
   const bool ok = axis(grid.x, block.x) && axis(grid.y, block.y) && axis(grid.z, block.z) &&
-                  block.x * block.y * block.z <= 1024 && grid.y <= 65535 && grid.z <= 65535 && lds <= 65536;
+                  block.x * block.y * block.z <= 1024 && grid.y <= 65535 && grid.z <= 65535 && lds <= 65536 && launches.size() != fail_at;
   Launch l{names().at(f), grid, block, ok ? hipSuccess : hipErrorInvalidConfiguration};
   if (ok && on_launch != nullptr) on_launch(l, args);
   launches.push_back(l);
@@ -141,9 +144,97 @@ static void sort() {
           }
 }
 
+// Every operator in every sequence of launches.
+struct Call {
+  const char* name;
+  std::function<tide_status()> run;
+};
+static std::vector<Call> calls() {
+  std::vector<Call> c;
+  static std::vector<const void*> grads;
+  static std::vector<void*> outs;
+  static std::vector<int64_t> few(300, 1), some(100, 100000), many(300, 1000000);
+  if (grads.empty())
+    for (int i = 0; i < 300; ++i) {
+      grads.push_back(reinterpret_cast<void*>((uintptr_t(1) << 40) + (uintptr_t(i) << 30)));
+      outs.push_back(const_cast<void*>(grads.back()));
+    }
+  double* sumsq = static_cast<double*>(at(2));
+  float* norm = static_cast<float*>(at(3));
+  for (const std::vector<int64_t>* n : {&few, &some, &many}) {
+    const int32_t count = int32_t(n->size());
+    c.push_back({"grad_norm", [=] {
+                   return tide_grad_norm(count, grads.data(), n->data(), TIDE_BF16, sumsq, norm, at(4), kWorkspace, nullptr);
+                 }});
+    c.push_back({"grad_clip", [=] {
+                   return tide_grad_clip(count, grads.data(), outs.data(), n->data(), TIDE_FP32, sumsq, 1.0, norm, nullptr);
+                 }});
+    c.push_back({"clip_grad_norm", [=] {
+                   return tide_clip_grad_norm(count, grads.data(), outs.data(), n->data(), TIDE_FP32, 1.0, sumsq, norm,
+                                              at(4), kWorkspace, nullptr);
+                 }});
+  }
+  const auto ln = [](int64_t rows, int64_t cols) {
+    return tide_layer_norm(rows, cols, at(1), cols, TIDE_BF16, at(2), at(3), TIDE_BF16, 1e-5f, at(4), cols,
+                           static_cast<float*>(at(5)), static_cast<float*>(at(6)), nullptr);
+  };
+  const auto ln_bwd = [](int64_t rows, int64_t cols, bool in_place) {
+    return tide_layer_norm_bwd(rows, cols, at(1), cols, at(2), cols, TIDE_BF16, at(3), TIDE_FP32,
+                               static_cast<float*>(at(4)), static_cast<float*>(at(5)), in_place ? at(1) : at(6), cols,
+                               at(7), at(8), at(9), kWorkspace, nullptr);
+  };
+  for (int64_t cols : {40, 4096, 16384, 40000})
+    for (int64_t rows : {3, 5000}) {
+      c.push_back({"layer_norm", [=] { return ln(rows, cols); }});
+      for (bool in_place : {false, true}) c.push_back({"layer_norm_bwd", [=] { return ln_bwd(rows, cols, in_place); }});
+    }
+  for (int64_t tokens : {40, 600, 5000})
+    for (int64_t vocab : {int64_t(100), int64_t(200000), (int64_t(1) << 31) - 1}) {
+      c.push_back({"embedding", [=] {
+                     return tide_embedding(tokens, at(1), TIDE_INT32, vocab, 700, at(2), TIDE_FP32, 1.0f, at(3), nullptr);
+                   }});
+      for (int accumulate : {0, 1})
+        c.push_back({"embedding_bwd", [=] { return table_gradient(tokens, vocab, 700, TIDE_FP32, TIDE_INT32, accumulate); }});
+    }
+  return c;
+}
+
+static void failed() {
+  size_t most = 0;
+  for (const Call& c : calls()) {
+    launches.clear();
+    CHECK(c.run() == TIDE_OK, "%s: %s", c.name, describe().c_str());
+    const size_t n = launches.size();
+    most = std::max(most, n);
+    for (size_t k = 0; k < n; ++k) {
+      launches.clear();
+      fail_at = k;
+      CHECK(c.run() == TIDE_ERR_HIP, "%s", c.name);
+      fail_at = SIZE_MAX;
+      CHECK(launches.size() == k + 1, "%s goes on after launch %zu of %zu: %s", c.name, k + 1, n, describe().c_str());
+      CHECK(tide_step_last_hip_error() == hipErrorInvalidConfiguration, "%s", c.name);
+      CHECK(last_error == hipSuccess, "%s leaves its own error", c.name);
+      last_error = hipSuccess;
+    }
+  }
+  CHECK(most >= 5, "%zu", most);  // zeros, two sorts, sums, join
+}
+
+static void stale() {
+  for (const Call& c : calls()) {
+    launches.clear();
+    last_error = hipErrorNotReady;
+    CHECK(c.run() == TIDE_OK, "%s reports another call's error", c.name);
+    CHECK(last_error == hipErrorNotReady, "%s clears another call's error", c.name);
+    last_error = hipSuccess;
+  }
+}
+
 int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "sort") sort();
+  else if (what == "failed") failed();
+  else if (what == "stale") stale();
   else ++failures;
   std::printf("%d failures\n", failures);
   return failures == 0 ? 0 : 1;
