@@ -565,30 +565,33 @@ __global__ __launch_bounds__(64) void layer_norm_bwd_cols_kernel(LayerNormBwdArg
   store_vec<float, E, false, false>(part + padded(D) + c, n, db);
 }
 
-// Adds the workgroups' partial sums: a workgroup takes 64 columns, a thread four of them and every
-// sixteenth partial; the sixteen sums of a column meet in LDS, in order.
+// Adds the workgroups' partial sums: a workgroup takes 64 columns (and those a grid further), a thread four
+// of them and every sixteenth partial; the sixteen sums of a column meet in LDS, in order.
 template <typename PT>
 __global__ __launch_bounds__(256) void layer_norm_join_kernel(const float* __restrict__ partial, int groups, int64_t D,
                                                               PT* dweight, PT* dbias) {
   __shared__ float lds[16][64];
   const int64_t P = padded(D);
   const int slice = threadIdx.x >> 4, q = (threadIdx.x & 15) * 4;
-  const int64_t c = int64_t(blockIdx.x) * 64 + q;  // of the 2 * P columns
-  f32x4 s = {0, 0, 0, 0};
-  if (c < 2 * P) {
+  for (int64_t b = blockIdx.x; b * 64 < 2 * P; b += gridDim.x) {
+    if (b != int64_t(blockIdx.x)) __syncthreads();  // the last columns' sums are read
+    const int64_t c = b * 64 + q;                   // of the 2 * P columns
+    f32x4 s = {0, 0, 0, 0};
+    if (c < 2 * P) {
 #pragma unroll 8
-    for (int g = slice; g < groups; g += 16) s += __builtin_bit_cast(f32x4, load16(partial + int64_t(g) * 2 * P + c));
-  }
-  *reinterpret_cast<f32x4*>(&lds[slice][q]) = s;
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int64_t o = int64_t(blockIdx.x) * 64 + threadIdx.x, col = o < P ? o : o - P;
-    PT* out = o < P ? dweight : dbias;
-    if (o < 2 * P && col < D && out != nullptr) {
-      float t = 0;
+      for (int g = slice; g < groups; g += 16) s += __builtin_bit_cast(f32x4, load16(partial + int64_t(g) * 2 * P + c));
+    }
+    *reinterpret_cast<f32x4*>(&lds[slice][q]) = s;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      const int64_t o = b * 64 + threadIdx.x, col = o < P ? o : o - P;
+      PT* out = o < P ? dweight : dbias;
+      if (o < 2 * P && col < D && out != nullptr) {
+        float t = 0;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) t += lds[k][threadIdx.x];
-      out[col] = narrow<PT>(t);
+        for (int k = 0; k < 16; ++k) t += lds[k][threadIdx.x];
+        out[col] = narrow<PT>(t);
+      }
     }
   }
 }
@@ -724,8 +727,8 @@ int backward(LayerNormBwdArgs a, int groups, hipStream_t s) {
       return launch(layer_norm_bwd_wide_kernel<T, PT>, unsigned(min64(a.rows, kMaxGrid)), kWideThreads, 0, s, a);
     });
   if (e != 0 || !params) return e;
-  return launch(layer_norm_join_kernel<PT>, unsigned(ceil_div(2 * padded(a.cols), 64)), 256, 0, s, a.partial, groups,
-                a.cols, static_cast<PT*>(a.dweight), static_cast<PT*>(a.dbias));
+  return launch(layer_norm_join_kernel<PT>, unsigned(min64(ceil_div(2 * padded(a.cols), 64), kMaxGrid)), 256, 0, s,
+                a.partial, groups, a.cols, static_cast<PT*>(a.dweight), static_cast<PT*>(a.dbias));
 }
 
 // Workgroups: as many as are resident at 16 waves a compute unit, each with at least two turns.

@@ -2,6 +2,7 @@
 // refuses what the runtime refuses, and looks at what each call launches.  Exit status 0 = all checks passed.
 //
 //   host_step_launches sort     table gradients up to the largest vocabulary that is accepted
+//   host_step_launches columns  layer norm and its gradient up to the widest row that is accepted
 //   host_step_launches failed   no kernel follows one that was not launched
 //   host_step_launches stale    an error of another library's earlier call is neither reported nor cleared
 #include <hip/hip_runtime_api.h>
@@ -144,6 +145,30 @@ static void sort() {
           }
 }
 
+static tide_status layer_norm(int64_t rows, int64_t cols, int dtype = TIDE_BF16) {
+  return tide_layer_norm(rows, cols, at(1), cols, dtype, at(2), at(3), TIDE_BF16, 1e-5f, at(4), cols,
+                         static_cast<float*>(at(5)), static_cast<float*>(at(6)), nullptr);
+}
+static tide_status layer_norm_bwd(int64_t rows, int64_t cols, bool in_place = false, int dtype = TIDE_BF16) {
+  return tide_layer_norm_bwd(rows, cols, at(1), cols, at(2), cols, dtype, at(3), TIDE_FP32, static_cast<float*>(at(4)),
+                             static_cast<float*>(at(5)), in_place ? at(1) : at(6), cols, at(7), at(8), at(9), kWorkspace,
+                             nullptr);
+}
+
+static void columns() {
+  for (int64_t cols : {int64_t(1), int64_t(40), int64_t(40000), int64_t(1) << 25, int64_t(1) << 28,
+                       (int64_t(1) << 29) - 4, int64_t(1) << 29, int64_t(1) << 30, (int64_t(1) << 31) - 1})
+    for (int64_t rows : {0, 1, 16, 17, 1000})
+      for (int dtype : {TIDE_BF16, TIDE_FP32}) {
+        launches.clear();
+        CHECK(layer_norm(rows, cols, dtype) == TIDE_OK, "%lld x %lld: %s", (long long)rows, (long long)cols,
+              describe().c_str());
+        launches.clear();
+        CHECK(layer_norm_bwd(rows, cols, false, dtype) == TIDE_OK, "%lld x %lld: %s", (long long)rows, (long long)cols,
+              describe().c_str());
+      }
+}
+
 // Every operator in every sequence of launches.
 struct Call {
   const char* name;
@@ -174,19 +199,11 @@ static std::vector<Call> calls() {
                                               at(4), kWorkspace, nullptr);
                  }});
   }
-  const auto ln = [](int64_t rows, int64_t cols) {
-    return tide_layer_norm(rows, cols, at(1), cols, TIDE_BF16, at(2), at(3), TIDE_BF16, 1e-5f, at(4), cols,
-                           static_cast<float*>(at(5)), static_cast<float*>(at(6)), nullptr);
-  };
-  const auto ln_bwd = [](int64_t rows, int64_t cols, bool in_place) {
-    return tide_layer_norm_bwd(rows, cols, at(1), cols, at(2), cols, TIDE_BF16, at(3), TIDE_FP32,
-                               static_cast<float*>(at(4)), static_cast<float*>(at(5)), in_place ? at(1) : at(6), cols,
-                               at(7), at(8), at(9), kWorkspace, nullptr);
-  };
   for (int64_t cols : {40, 4096, 16384, 40000})
     for (int64_t rows : {3, 5000}) {
-      c.push_back({"layer_norm", [=] { return ln(rows, cols); }});
-      for (bool in_place : {false, true}) c.push_back({"layer_norm_bwd", [=] { return ln_bwd(rows, cols, in_place); }});
+      c.push_back({"layer_norm", [=] { return layer_norm(rows, cols); }});
+      for (bool in_place : {false, true})
+        c.push_back({"layer_norm_bwd", [=] { return layer_norm_bwd(rows, cols, in_place); }});
     }
   for (int64_t tokens : {40, 600, 5000})
     for (int64_t vocab : {int64_t(100), int64_t(200000), (int64_t(1) << 31) - 1}) {
@@ -233,6 +250,7 @@ static void stale() {
 int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "sort") sort();
+  else if (what == "columns") columns();
   else if (what == "failed") failed();
   else if (what == "stale") stale();
   else ++failures;

@@ -5,8 +5,8 @@ import weakref
 import pytest
 import torch
 
-from all_gather_placement_amd import TideError, clip_grad_norm, embedding_bwd, grad_clip, grad_norm, load_step_binding
-from test_gpu_step import BF16, FP32, gen, normal, say, whole
+from all_gather_placement_amd import TideError, clip_grad_norm, embedding_bwd, grad_clip, grad_norm, layer_norm_bwd, load_step_binding
+from test_gpu_step import BF16, FP32, gen, normal, say, uo, whole, within
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,21 @@ def test_table_gradient_of_more_rows_than_one_launch_sorts(gpu_available, vocab)
     embedding_bwd(ids, dy, vocab, out=grad, accumulate=True)
     assert torch.equal(grad[rows], (want + want.float().bfloat16().double()).float().bfloat16())
     assert int(torch.count_nonzero(grad)) == rows.numel()
+
+
+@pytest.mark.parametrize("cols", [(1 << 29) + 5, (1 << 29) + 4096])
+def test_parameter_gradients_of_more_columns_than_one_launch_joins(gpu_available, cols):
+    say("row of many columns", cols)
+    x, dy = whole((1, cols), BF16, 1, -2, 3), whole((1, cols), BF16, 2, -2, 3)
+    stat = torch.zeros(1, device="cuda")
+    dw, db = torch.full((2, cols), float("nan"), dtype=BF16, device="cuda")
+    dx, _, _ = layer_norm_bwd(dy, x, None, stat, stat + 1, dweight=dw, dbias=db)
+    # one row of whole numbers, mean 0 and rstd 1: products of fp32 are exact, and fit bf16
+    assert torch.equal(dw, (x * dy)[0]) and torch.equal(db, dy[0])
+    # a thread's sums stay below 2^24; ten additions of sums of at most 4 a column follow, and three operations
+    m1 = float(dy.sum(dtype=torch.float64)) / cols
+    m2 = float((x * dy).sum(dtype=torch.float64)) / cols
+    for part in (slice(0, 1 << 20), slice(cols - (1 << 20), cols)):
+        want = dy[0, part].double() - m1 - x[0, part].double() * m2
+        tol = 16 * 2.0 ** -24 * 24
+        within(dx[0, part], want, tol + uo(BF16) * (want.abs() + tol), "dx")
