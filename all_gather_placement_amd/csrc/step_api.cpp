@@ -35,6 +35,7 @@ inline Range range_of(const void* p, int64_t bytes) {
 inline Range range_of(const void* p, int64_t rows, int64_t row, int64_t stride, int size) {
   return range_of(p, rows == 0 ? 0 : ((rows - 1) * stride + row) * size);
 }
+inline Range opt_range(const void* p, int64_t bytes) { return p == nullptr ? Range{0, 0} : range_of(p, bytes); }
 inline bool overlap(const Range& a, const Range& b) {
   return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi;
 }
@@ -227,6 +228,20 @@ bool clip_overlaps(int32_t n, const void* const* grads, void* const* outs, const
   return false;
 }
 
+// Whether one of the results or the workspace lies over another or over a gradient: a workgroup would write
+// what others still read.
+template <size_t N>
+bool results_overlap(const Range (&results)[N], int32_t n, const void* const* grads, const int64_t* numels, int dtype) {
+  const Range none[] = {{0, 0}};
+  if (outputs_overlap(results, none)) return true;
+  for (int32_t i = 0; i < n; ++i) {
+    const Range g = range_of(grads[i], numels[i] * size_of(dtype));
+    for (const Range& r : results)
+      if (overlap(r, g)) return true;
+  }
+  return false;
+}
+
 bool max_norm_ok(double m) { return m >= 0; }  // false for NaN
 
 }  // namespace
@@ -244,8 +259,12 @@ int64_t tide_grad_norm_workspace(int32_t num_tensors, const int64_t* numels, int
 tide_status tide_grad_norm(int32_t num_tensors, const void* const* grads, const int64_t* numels, int32_t dtype,
                            double* sumsq, float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!tensors_ok(num_tensors, numels, dtype) || !pointers_ok(num_tensors, grads, numels, dtype) ||
-      !aligned(sumsq, 8) || !aligned(norm, 4) ||
-      !workspace_ok(workspace, workspace_bytes, norm_workspace(num_tensors, numels, dtype)))
+      !aligned(sumsq, 8) || !aligned(norm, 4))
+    return TIDE_ERR_INVALID;
+  const int64_t need = norm_workspace(num_tensors, numels, dtype);
+  const Range results[] = {opt_range(sumsq, 8), opt_range(norm, 4), opt_range(workspace, need)};
+  if (!workspace_ok(workspace, workspace_bytes, need) ||
+      results_overlap(results, num_tensors, grads, numels, dtype))
     return TIDE_ERR_INVALID;
   return status_of(enqueue_norm(num_tensors, grads, numels, dtype, sumsq, norm, workspace, stream));
 }
@@ -256,9 +275,10 @@ tide_status tide_grad_clip(int32_t num_tensors, const void* const* grads, void* 
       !pointers_ok(num_tensors, const_cast<const void* const*>(outs), numels, dtype) || sumsq == nullptr ||
       !aligned(sumsq, 8) || !aligned(norm, 4) || !max_norm_ok(max_norm))
     return TIDE_ERR_INVALID;
-  std::vector<Range> scalars{range_of(sumsq, 8)};
-  if (norm != nullptr) scalars.push_back(range_of(norm, 4));
-  if (clip_overlaps(num_tensors, grads, outs, numels, dtype, scalars)) return TIDE_ERR_INVALID;
+  const Range sum = range_of(sumsq, 8), results[] = {opt_range(norm, 4)};
+  if (overlap(results[0], sum) || results_overlap(results, num_tensors, grads, numels, dtype) ||
+      clip_overlaps(num_tensors, grads, outs, numels, dtype, {sum, results[0]}))
+    return TIDE_ERR_INVALID;
   return status_of(enqueue_clip(num_tensors, grads, outs, numels, dtype, sumsq, nullptr, nullptr, 0, max_norm, norm, stream));
 } catch (const std::bad_alloc&) {
   return TIDE_ERR_NOMEM;
@@ -273,10 +293,10 @@ tide_status tide_clip_grad_norm(int32_t num_tensors, const void* const* grads, v
     return TIDE_ERR_INVALID;
   const int64_t need = norm_workspace(num_tensors, numels, dtype);
   if (!workspace_ok(workspace, workspace_bytes, need)) return TIDE_ERR_INVALID;
-  std::vector<Range> scalars{range_of(workspace, need)};
-  if (sumsq != nullptr) scalars.push_back(range_of(sumsq, 8));
-  if (norm != nullptr) scalars.push_back(range_of(norm, 4));
-  if (clip_overlaps(num_tensors, grads, outs, numels, dtype, scalars)) return TIDE_ERR_INVALID;
+  const Range results[] = {opt_range(sumsq, 8), opt_range(norm, 4), range_of(workspace, need)};
+  if (results_overlap(results, num_tensors, grads, numels, dtype) ||
+      clip_overlaps(num_tensors, grads, outs, numels, dtype, {results[0], results[1], results[2]}))
+    return TIDE_ERR_INVALID;
   double* s = sumsq != nullptr ? sumsq : static_cast<double*>(workspace);
   const int64_t chunks = num_chunks(num_tensors, numels, dtype);
   if (one_workgroup(chunks))
@@ -318,7 +338,6 @@ bool strided_ok(const void* p, int64_t rows, int64_t cols, int64_t stride, int d
   return p != nullptr && aligned(p, size_of(dtype)) && (rows == 1 || (stride >= cols && stride <= kMaxElems / rows));
 }
 bool vector_ok(const void* p, int dtype) { return aligned(p, size_of(dtype)); }
-inline Range opt_range(const void* p, int64_t bytes) { return p == nullptr ? Range{0, 0} : range_of(p, bytes); }
 
 int64_t layer_norm_bwd_bytes(int64_t rows, int64_t cols, int dtype) {
   return int64_t(layer_norm_bwd_groups(rows, cols, dtype)) * 2 * layer_norm_bwd_padded(cols) * 4;

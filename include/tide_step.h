@@ -60,7 +60,8 @@ enum {
  * infinity anywhere gives NaN or infinity.  A data-parallel job adds up `sumsq` over its ranks and
  * passes the total to tide_grad_clip.
  * Errors: TIDE_ERR_INVALID (null or misaligned pointer, negative count, unknown dtype, total above
- * 2^42 elements, workspace too small or misaligned), TIDE_ERR_HIP.
+ * 2^42 elements, workspace too small or misaligned, sumsq, norm or workspace over a gradient or each
+ * other), TIDE_ERR_HIP.
  */
 int64_t tide_grad_norm_workspace(int32_t num_tensors, const int64_t* numels, int32_t dtype); /* bytes; -1: bad argument */
 tide_status tide_grad_norm(int32_t num_tensors, const void* const* grads, const int64_t* numels, int32_t dtype,
@@ -72,11 +73,12 @@ tide_status tide_grad_norm(int32_t num_tensors, const void* const* grads, const 
  *   max_norm  >= 0, may be infinity, not NaN
  *   outs      host [num_tensors]: where tensor i goes, contiguous, of the gradients' type; outs[i] may
  *             be grads[i] (in place) and must otherwise not overlap any gradient or output
- *   norm      device, one float, or NULL
+ *   norm      device, one float, or NULL; not within a gradient, output or *sumsq
  * Result: with n = sqrt(sumsq) and c = min(1, max_norm / (n + 1e-6)) in 64 bits, rounded to fp32,
  * outs[i][k] = grads[i][k] * c, one fp32 product rounded to the tensors' type; norm = n.  A NaN or
  * infinite n gives c = NaN or 0 (NaN where max_norm is infinite too), as the formula says.
- * Errors: as tide_grad_norm; TIDE_ERR_INVALID also for overlaps and a max_norm below 0 or NaN.
+ * Errors: as tide_grad_norm; TIDE_ERR_INVALID also for overlaps and a max_norm below 0 or NaN,
+ * TIDE_ERR_NOMEM where the host has no memory for the check of overlaps.
  */
 tide_status tide_grad_clip(int32_t num_tensors, const void* const* grads, void* const* outs, const int64_t* numels,
                            int32_t dtype, const double* sumsq, double max_norm, float* norm, void* stream);

@@ -3,6 +3,7 @@
 //
 //   host_step_launches sort     table gradients up to the largest vocabulary that is accepted
 //   host_step_launches columns  layer norm and its gradient up to the widest row that is accepted
+//   host_step_launches scalars  norm, sum of squares and workspace over a gradient, an output or each other
 //   host_step_launches failed   no kernel follows one that was not launched
 //   host_step_launches stale    an error of another library's earlier call is neither reported nor cleared
 #include <hip/hip_runtime_api.h>
@@ -169,6 +170,81 @@ static void columns() {
       }
 }
 
+// Refused before anything is launched, or not at all.
+static void expect(bool refused, tide_status s, const char* what, int64_t where) {
+  CHECK((s == TIDE_ERR_INVALID) == refused && (refused ? launches.empty() : s == TIDE_OK), "%s %lld: status %d, %zu launches",
+        what, (long long)where, int(s), launches.size());
+  launches.clear();
+}
+
+static void scalars() {
+  // two gradients of 1000 floats, outputs elsewhere, one long list
+  char* base = static_cast<char*>(at(1));
+  char* far = static_cast<char*>(at(2));
+  const int64_t numels[] = {1000, 1000};
+  const void* grads[] = {base, base + 8192};
+  void* outs[] = {base + 65536, base + 65536 + 8192};
+  void* same[] = {base, base + 8192};
+  const int64_t need = tide_grad_norm_workspace(2, numels, TIDE_FP32);
+  const auto f64 = [](char* p) { return reinterpret_cast<double*>(p); };
+  const auto f32 = [](char* p) { return reinterpret_cast<float*>(p); };
+  const auto norm = [&](char* sumsq, char* value, char* ws) {
+    launches.clear();
+    return tide_grad_norm(2, grads, numels, TIDE_FP32, f64(sumsq), f32(value), ws, need, nullptr);
+  };
+  const auto clip = [&](void* const* to, char* sumsq, char* value) {
+    launches.clear();
+    return tide_grad_clip(2, grads, to, numels, TIDE_FP32, f64(sumsq), 1.0, f32(value), nullptr);
+  };
+  const auto both = [&](void* const* to, char* sumsq, char* value, char* ws) {
+    launches.clear();
+    return tide_clip_grad_norm(2, grads, to, numels, TIDE_FP32, 1.0, f64(sumsq), f32(value), ws, need, nullptr);
+  };
+  // where 4, 8 and `need` bytes lie over one of the gradients, of 4000 bytes each
+  for (int64_t o : {0, 16, 3984, 8192, 8192 + 3984, 8192 + 2000 - 2000 % 16}) {
+    char* p = base + o;
+    expect(true, norm(nullptr, p, far), "norm over a gradient", o);
+    expect(true, norm(p, nullptr, far), "sum over a gradient", o);
+    expect(true, norm(nullptr, nullptr, p), "workspace over a gradient", o);
+    expect(true, clip(outs, far, p), "clip: norm over a gradient", o);
+    expect(false, clip(outs, p, far), "clip: the given sum may be part of a gradient that is not written", o);
+    expect(true, clip(same, p, far), "clip: the given sum over an output", o);
+    for (void* const* to : {outs, same}) {
+      expect(true, both(to, nullptr, p, far), "norm and clip: norm over a gradient", o);
+      expect(true, both(to, p, nullptr, far), "norm and clip: sum over a gradient", o);
+      expect(true, both(to, nullptr, nullptr, p), "norm and clip: workspace over a gradient", o);
+    }
+  }
+  for (int64_t o : {-64, 4000, 8192 + 4000}) {  // beside them
+    char* p = base + o;
+    expect(false, norm(nullptr, p, far), "norm beside a gradient", o);
+    expect(false, norm(p, nullptr, far), "sum beside a gradient", o);
+    expect(false, clip(outs, far, p), "clip: norm beside a gradient", o);
+    expect(false, both(outs, nullptr, p, far), "norm and clip: norm beside a gradient", o);
+    expect(false, both(same, p, nullptr, far), "norm and clip: sum beside a gradient", o);
+  }
+  expect(true, norm(base - 32, nullptr, base - need + 8), "workspace's end over a gradient", 0);
+  // each other: a norm in either half of the sum of squares, either of them in the workspace
+  for (int64_t o : {0, 4}) {
+    expect(true, norm(far, far + o, far + 4096), "norm in the sum", o);
+    expect(true, clip(outs, far, far + o), "clip: norm in the given sum", o);
+    expect(true, clip(same, far, far + o), "clip in place: norm in the given sum", o);
+    expect(true, both(outs, far, far + o, far + 4096), "norm and clip: norm in the sum", o);
+  }
+  for (int64_t o : {int64_t(0), int64_t(8), need - 8}) {
+    expect(true, norm(far + o, nullptr, far), "sum in the workspace", o);
+    expect(true, norm(nullptr, far + o, far), "norm in the workspace", o);
+    expect(true, both(same, far + o, nullptr, far), "norm and clip: sum in the workspace", o);
+    expect(true, both(outs, nullptr, far + o, far), "norm and clip: norm in the workspace", o);
+  }
+  expect(false, norm(far, far + 8, far + 16), "next to each other", 0);
+  expect(false, clip(outs, far, far + 8), "next to each other", 1);
+  expect(false, both(same, far, far + 8, far + 16), "next to each other", 2);
+  const int64_t none[] = {0, 0};
+  expect(false, tide_grad_norm(2, grads, none, TIDE_FP32, f64(base), f32(base + 8192), far, need, nullptr),
+         "gradients without elements lie over nothing", 0);
+}
+
 // Every operator in every sequence of launches.
 struct Call {
   const char* name;
@@ -251,6 +327,7 @@ int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "sort") sort();
   else if (what == "columns") columns();
+  else if (what == "scalars") scalars();
   else if (what == "failed") failed();
   else if (what == "stale") stale();
   else ++failures;
