@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import hashlib
+import importlib.util
 import os
 import re
 import shutil
@@ -134,12 +135,30 @@ def check_current(lib: str = LIB, loaded=None) -> None:
                            f"rebuild it: python -m all_gather_placement_amd.build")
 
 
+def has_torch() -> bool:
+    """Whether the Python module can be built; the libraries' C ABI needs no torch."""
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except (ImportError, ValueError):
+        return False
+
+
 def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, probe: bool = True) -> str:
-    """Compile every source and link the shared library (and the step and probe libraries); returns its path."""
+    """Compile every source and link the shared library, then the probe and step libraries and, where torch
+    is installed, the step operators' Python module; returns the first one's path."""
+    compile_library(out, sources, verbose, extra)
     if probe and out == LIB:
-        build(verbose=verbose, extra=extra, out=PROBE_LIB, sources=PROBE_SOURCES, probe=False)
-        build(verbose=verbose, extra=extra, out=STEP_LIB, sources=STEP_SOURCES, probe=False)
-        build(verbose=verbose, extra=extra, out=STEP_BINDING, sources=STEP_BINDING_SOURCES, probe=False)
+        compile_library(PROBE_LIB, PROBE_SOURCES, verbose, extra)
+        compile_library(STEP_LIB, STEP_SOURCES, verbose, extra)
+        if has_torch():
+            compile_library(STEP_BINDING, STEP_BINDING_SOURCES, verbose, extra)
+        else:
+            print(f"torch is not installed: {os.path.basename(STEP_BINDING)} is not built", flush=True)
+    return out
+
+
+def compile_library(out: str, sources, verbose: bool = False, extra=()) -> None:
+    """Compile `sources` and link them to `out`."""
     objdir = os.path.join(PKG, "_build", os.path.splitext(os.path.basename(out))[0])
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
@@ -173,7 +192,6 @@ def build(verbose: bool = False, extra=(), out: str = LIB, sources=SOURCES, prob
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(tmp, out)
-    return out
 
 
 def is_current(lib: str) -> bool:
@@ -190,7 +208,7 @@ def is_current(lib: str) -> bool:
 def ensure_built(verbose: bool = False) -> str:
     """Build the libraries if they are missing or were built from other sources (tests, smoke and
     benchmark entry points); returns the path of libtide.so."""
-    if not all(map(is_current, (LIB, PROBE_LIB, STEP_LIB, STEP_BINDING))):
+    if not all(map(is_current, (LIB, PROBE_LIB, STEP_LIB, *((STEP_BINDING,) if has_torch() else ())))):
         build(verbose=verbose)
     return LIB
 

@@ -83,7 +83,8 @@ def load_step_binding():
         from .build import STEP_BINDING, check_current
 
         if not os.path.exists(STEP_BINDING):
-            raise RuntimeError(f"{STEP_BINDING} is not built; run `python -m all_gather_placement_amd.build`")
+            raise RuntimeError(f"{STEP_BINDING} is not built; run `python -m all_gather_placement_amd.build` where "
+                               "torch is installed")
         check_current(STEP_BINDING)
         from . import _step as module
 
