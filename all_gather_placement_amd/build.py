@@ -9,7 +9,7 @@ used, so fp32 denormals and rounding are IEEE.
 
 Each library embeds a build id: the first 16 hex digits of the SHA-256 of its sources, the headers
 they include and the compile flags (``tide_build_id()`` / ``tide_step_build_id()`` /
-``tide_probe_build_id()``).
+``tide_probe_build_id()``); the Python module's also covers the torch and the interpreter it is made for.
 :func:`ensure_built` rebuilds a library whose embedded id differs from the sources in the tree, and
 the bindings refuse to load one, so a library built from other sources is never run.
 """
@@ -77,9 +77,24 @@ def source_hash(lib: str = LIB, extra=()) -> str:
             h.update(fh.read())
         h.update(b"\0")
     h.update(" ".join(compile_flags(extra)).replace(INCLUDE, "<include>").encode())
+    if lib == STEP_BINDING:
+        h.update(b"\0" + module_target())
     return h.hexdigest()[:16]
 
 
+def module_target() -> bytes:
+    """What the Python module is compiled against: the interpreter's ABI, torch's version (and revision
+    and HIP version, from the file that states them, so that torch is not loaded) and the flags that name
+    no place."""
+    spec = importlib.util.find_spec("torch") if has_torch() else None
+    version = b""
+    if spec is not None:
+        with open(os.path.join(spec.submodule_search_locations[0], "version.py"), "rb") as fh:
+            version = fh.read()
+    return b"\0".join((str(sysconfig.get_config_var("SOABI")).encode(), version, " ".join(MODULE_FLAGS).encode()))
+
+
+MODULE_FLAGS = ["-fvisibility=hidden"]
 BINDING_MARK = rb"tide_step_binding build id ([0-9a-f]{16})\0"
 
 
@@ -88,7 +103,7 @@ def torch_flags() -> list:
     from torch.utils.cpp_extension import include_paths
 
     dirs = [*include_paths(), sysconfig.get_paths()["include"]]
-    return ["-fvisibility=hidden", *(f for d in dirs for f in ("-isystem", d))]
+    return [*MODULE_FLAGS, *(f for d in dirs for f in ("-isystem", d))]
 
 
 def torch_link_flags() -> list:

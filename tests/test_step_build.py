@@ -1,6 +1,9 @@
 """Building the libraries: the collectives' does not depend on the step operators' Python module."""
 import importlib.util
+import os
 import subprocess
+import sysconfig
+from types import SimpleNamespace
 
 import pytest
 
@@ -53,3 +56,36 @@ def test_the_collectives_are_built_where_the_module_is_not(linked):
     with pytest.raises(subprocess.CalledProcessError):
         build.build()
     assert made == [build.LIB, build.PROBE_LIB, build.STEP_LIB]
+
+
+def test_the_modules_build_id_covers_torch_and_the_interpreter(monkeypatch, tmp_path):
+    """Its compiled code fits one torch and one interpreter; the libraries' code depends on neither."""
+    libs = (build.LIB, build.PROBE_LIB, build.STEP_LIB)
+    ids, module = [build.source_hash(lib) for lib in libs], build.source_hash(build.STEP_BINDING)
+    assert build.built_id(build.STEP_BINDING) == module
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    (tmp_path / "version.py").write_bytes(open(os.path.join(torch, "version.py"), "rb").read())
+    found = importlib.util.find_spec
+    there = SimpleNamespace(submodule_search_locations=[str(tmp_path)])
+    seen = {module}
+
+    def changed():
+        assert [build.source_hash(lib) for lib in libs] == ids
+        now = build.source_hash(build.STEP_BINDING)
+        new = now not in seen
+        seen.add(now)
+        return new
+
+    with monkeypatch.context() as m:
+        m.setattr(importlib.util, "find_spec", lambda name, *a: there if name == "torch" else found(name, *a))
+        assert not changed()  # the same torch elsewhere
+        (tmp_path / "version.py").write_text("__version__ = '99.0'\n")
+        assert changed()
+        assert not build.is_current(build.STEP_BINDING)
+    config = sysconfig.get_config_var
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-999" if name == "SOABI" else config(name))
+        assert changed()
+    with monkeypatch.context() as m:
+        m.setattr(build, "MODULE_FLAGS", ["-O1"])
+        assert changed()
