@@ -141,6 +141,11 @@ struct Workspace {
   }
 };
 
+// Tells autograd that a caller's tensor was written in place: what saved it for a backward pass refuses to
+// use it.  Tensors of inference mode are not counted.
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 // What the caller passed, or what was made in its place.
 struct Output {
@@ -154,8 +159,9 @@ struct Output {
       t = &made;
     }
   }
-  PyObject* result() const {
+  PyObject* result() const {  // of a call that has been enqueued
     if (given == Py_None) return wrap(made);
+    changed(*t);
     Py_INCREF(given);
     return given;
   }
@@ -196,6 +202,10 @@ struct List {
   std::vector<int64_t> n;
   at::ScalarType type = at::kFloat;
   int32_t count() const { return int32_t(p.size()); }
+  void all_changed() const {
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(held.o); ++i)
+      changed(THPVariable_Unpack(PySequence_Fast_GET_ITEM(held.o, i)));
+  }
 
   List(const Device& d, PyObject* o, const char* name) : held(PySequence_Fast(o, "a sequence of tensors is wanted")) {
     PyObject* seq = held.o;
@@ -263,6 +273,7 @@ PyObject* grad_norm(Args a, Py_ssize_t n) {
   check(tide_grad_norm(g.count(), g.p.data(), g.n.data(), type, static_cast<double*>(at_of(sumsq)),
                        static_cast<float*>(at_of(norm.t)), ws.p, ws.bytes, d.stream()),
         "tide_grad_norm");
+  if (sumsq != nullptr) changed(*sumsq);
   return norm.result();
 }
 
@@ -282,6 +293,7 @@ PyObject* grad_clip(Args a, Py_ssize_t n) {
                        static_cast<double*>(sumsq.data_ptr()), max_norm, static_cast<float*>(at_of(norm.t)),
                        d.stream()),
         "tide_grad_clip");
+  outs.all_changed();
   return norm.result();
 }
 
@@ -304,6 +316,8 @@ PyObject* clip_grad_norm(Args a, Py_ssize_t n) {
                             static_cast<double*>(at_of(sumsq)), static_cast<float*>(at_of(norm.t)), ws.p, ws.bytes,
                             d.stream()),
         "tide_clip_grad_norm");
+  outs.all_changed();
+  if (sumsq != nullptr) changed(*sumsq);
   return norm.result();
 }
 

@@ -10,6 +10,10 @@ for what the library refuses.  There is no fallback: if the library is missing, 
 The functions here are the documentation of a compiled module, ``_step.so``, which checks and allocates;
 it calls the C ABI of the library that :func:`load_step_library` loads.
 
+Gradients are calls of their own: no call is recorded by autograd, so what it returns has no history,
+whether or not its inputs require grad.  Outputs passed in count as written in place, as by torch's own
+in-place functions.
+
 A caller that passes its own buffers and a stream other than the current one orders their use itself,
 as for any call on another stream.
 """

@@ -1,11 +1,11 @@
 """Calls of the training-step operators as a program makes them: lists that live only as long as the call,
-sizes beyond one launch."""
+sizes beyond one launch, outputs that autograd has saved."""
 import weakref
 
 import pytest
 import torch
 
-from all_gather_placement_amd import TideError, clip_grad_norm, embedding_bwd, grad_clip, grad_norm, layer_norm_bwd, load_step_binding
+from all_gather_placement_amd import TideError, clip_grad_norm, embedding, embedding_bwd, grad_clip, grad_norm, layer_norm, layer_norm_bwd, load_step_binding
 from test_gpu_step import BF16, FP32, gen, normal, say, uo, whole, within
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +133,68 @@ def test_parameter_gradients_of_more_columns_than_one_launch_joins(gpu_available
         want = dy[0, part].double() - m1 - x[0, part].double() * m2
         tol = 16 * 2.0 ** -24 * 24
         within(dx[0, part], want, tol + uo(BF16) * (want.abs() + tol), "dx")
+
+
+# ------------------------------------------------------------------------------------------------
+# Outputs and autograd
+# ------------------------------------------------------------------------------------------------
+
+def _calls():
+    """Every call with all of its outputs passed in: (call, inputs, outputs)."""
+    x, w = normal((6, 40), FP32, 1), normal((40,), FP32, 2)
+    y, mean, rstd = layer_norm(x, w)
+    ids, table = torch.tensor([1, 2, 1], device="cuda"), normal((9, 40), FP32, 3)
+    dy, dx, h = x.clone(), x.clone(), x[:3].clone()
+    dw, db, dtable = w.clone(), w.clone(), table.clone()
+    norm, total = torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.float64, device="cuda")
+    grads, outs = [x.clone(), w.clone(), w[:0]], [x.clone(), w.clone(), w[:0].clone()]
+    given = torch.ones(1, dtype=torch.float64, device="cuda")
+    return [
+        (lambda: layer_norm(x, w, out=y, mean=mean, rstd=rstd), [x, w], [y, mean, rstd]),
+        (lambda: layer_norm_bwd(dy, x, w, mean, rstd, dx=dx, dweight=dw, dbias=db), [dy, x, w, mean, rstd], [dx, dw, db]),
+        (lambda: layer_norm_bwd(dy, x, w, mean, rstd, dx=dy), [x, w, mean, rstd], [dy]),
+        (lambda: embedding(ids, table, out=h), [ids, table], [h]),
+        (lambda: embedding_bwd(ids, h, 9, out=dtable), [ids, h], [dtable]),
+        (lambda: embedding_bwd(ids, h, 9, out=dtable, accumulate=True), [ids, h], [dtable]),
+        (lambda: grad_norm(grads, norm=norm, sumsq=total), grads, [norm, total]),
+        (lambda: grad_clip(grads, given, 1.0, outs=outs, norm=norm), [*grads, given], [*outs, norm]),
+        (lambda: grad_clip(grads, given, 1.0), [given], grads),
+        (lambda: clip_grad_norm(grads, 1.0, outs=outs, norm=norm, sumsq=total), grads, [*outs, norm, total]),
+        (lambda: clip_grad_norm((g for g in grads), 1.0), [], grads),
+    ]
+
+
+def test_outputs_passed_in_count_as_written(gpu_available):
+    for i, (call, ins, outs) in enumerate(_calls()):
+        before = [t._version for t in (*ins, *outs)]
+        call()
+        after = [t._version for t in (*ins, *outs)]
+        assert after[:len(ins)] == before[:len(ins)], i
+        assert all(a > b for a, b in zip(after[len(ins):], before[len(ins):])), i
+    # refused calls write nothing
+    x = normal((4, 8), FP32, 1)
+    before = x._version
+    with pytest.raises(TideError):
+        layer_norm(x, out=x)
+    assert x._version == before
+
+
+def test_backward_refuses_what_was_written_over(gpu_available):
+    x = normal((4, 8), FP32, 1).requires_grad_()
+    saved = x.exp()
+    layer_norm(x, out=saved.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.sum().backward()
+    saved = x.exp()
+    clip_grad_norm([saved.detach()], 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.sum().backward()
+
+
+def test_outputs_of_inference_mode(gpu_available):
+    with torch.inference_mode():
+        for call, _, _ in _calls():
+            call()
+        kept = _calls()
+    for call, _, _ in kept:  # used outside it
+        call()
