@@ -26,6 +26,7 @@ inline int size_of(int t) { return t == TIDE_BF16 ? 2 : t == TIDE_INT64 ? 8 : 4;
 
 struct Range {
   uintptr_t lo, hi;
+  uintptr_t row = 0, stride = 0;  // bytes of each row and between rows' starts, where rows have gaps between them
 };
 inline Range range_of(const void* p, int64_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
@@ -33,11 +34,24 @@ inline Range range_of(const void* p, int64_t bytes) {
 }
 // `rows` rows of `row` elements, `stride` elements apart
 inline Range range_of(const void* p, int64_t rows, int64_t row, int64_t stride, int size) {
-  return range_of(p, rows == 0 ? 0 : ((rows - 1) * stride + row) * size);
+  Range r = range_of(p, rows == 0 ? 0 : ((rows - 1) * stride + row) * size);
+  if (rows > 1 && stride > row) {
+    r.row = uintptr_t(row * size);
+    r.stride = uintptr_t(stride * size);
+  }
+  return r;
 }
 inline Range opt_range(const void* p, int64_t bytes) { return p == nullptr ? Range{0, 0} : range_of(p, bytes); }
+// Blocks of columns of one buffer do not overlap though one's rows lie between the other's: of equal strides,
+// or of one whose gaps hold all of the other.  Rows of different strides are taken to meet somewhere.
 inline bool overlap(const Range& a, const Range& b) {
-  return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi;
+  if (!(a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi)) return false;
+  const uintptr_t stride = a.stride > b.stride ? a.stride : b.stride;
+  if (stride == 0 || (a.stride != b.stride && a.stride != 0 && b.stride != 0)) return true;
+  const uintptr_t arow = a.stride != 0 ? a.row : a.hi - a.lo, brow = b.stride != 0 ? b.row : b.hi - b.lo;
+  // where a row of a starts, counted from the row of b that starts at or before it
+  const uintptr_t from = a.lo >= b.lo ? (a.lo - b.lo) % stride : (stride - (b.lo - a.lo) % stride) % stride;
+  return from < brow || from + arow > stride;
 }
 // Whether any output lies over another output or an input; empty ranges lie over nothing.
 template <size_t N, size_t M>

@@ -19,7 +19,9 @@
  *   - `workspace` is caller-owned device memory of at least the bytes that the query of the same
  *     name gives, 16-byte aligned; its contents need no initialisation and mean nothing after the
  *     call.  Calls that may run at the same time need workspaces of their own.
- *   - Inputs are never written; outputs must not overlap inputs or each other unless stated.
+ *   - Inputs are never written; outputs must not overlap inputs or each other unless stated.  Blocks of
+ *     columns of one buffer, of one row stride, do not overlap; matrices of different row strides count
+ *     as overlapping where their first and last elements do.
  *   - Results do not depend on scheduling: sums have a fixed order for given sizes, and no
  *     floating-point atomic is used.
  *   - Errors are returned as tide_status, before any work is enqueued except TIDE_ERR_HIP; nothing

@@ -4,6 +4,7 @@
 //   host_step_launches sort     table gradients up to the largest vocabulary that is accepted
 //   host_step_launches columns  layer norm and its gradient up to the widest row that is accepted
 //   host_step_launches scalars  norm, sum of squares and workspace over a gradient, an output or each other
+//   host_step_launches blocks   blocks of columns of one buffer, as inputs and outputs
 //   host_step_launches failed   no kernel follows one that was not launched
 //   host_step_launches stale    an error of another library's earlier call is neither reported nor cleared
 #include <hip/hip_runtime_api.h>
@@ -245,6 +246,51 @@ static void scalars() {
          "gradients without elements lie over nothing", 0);
 }
 
+static void blocks() {
+  constexpr int64_t R = 5, S = 256;
+  char* base = static_cast<char*>(at(1));
+  // bf16 rows of `cols` elements from column `c` of a buffer with rows of S elements
+  const auto ln = [&](int64_t cols, int64_t xc, int64_t yc, int64_t ys, char* weight, char* mean) {
+    launches.clear();
+    return tide_layer_norm(R, cols, base + 2 * xc, S, TIDE_BF16, weight, nullptr, TIDE_BF16, 1e-5f, base + 2 * yc, ys,
+                           reinterpret_cast<float*>(mean), nullptr, nullptr);
+  };
+  const auto bwd = [&](int64_t cols, int64_t dyc, int64_t xc, int64_t dxc) {
+    launches.clear();
+    return tide_layer_norm_bwd(R, cols, base + 2 * dyc, S, base + 2 * xc, S, TIDE_BF16, nullptr, TIDE_BF16,
+                               static_cast<float*>(at(2)), static_cast<float*>(at(3)), base + 2 * dxc, S, at(4), at(5), at(6),
+                               kWorkspace, nullptr);
+  };
+  for (int64_t cols : {1, 7, 64, 128})
+    for (int64_t xc : {0, 3, 100})
+      for (int64_t yc = 0; yc < 2 * S; ++yc) {
+        // from element to element: the buffer's elements that either writes or reads
+        std::vector<int> used(size_t(R + 4) * S, 0);
+        for (int64_t r = 0; r < R; ++r)
+          for (int64_t c = 0; c < cols; ++c) used[size_t(xc + r * S + c)] = 1;
+        bool meet = false;
+        for (int64_t r = -1; r <= R; ++r)  // rows before and after count: a block is a block of all rows
+          for (int64_t c = 0; c < cols; ++c) {
+            const int64_t e = yc % S + r * S + c;
+            if (e >= 0) meet |= used[size_t(e)] != 0;
+          }
+        expect(meet, ln(cols, xc, yc, S, nullptr, nullptr), "blocks", yc);
+        expect(meet, bwd(cols, 2 * S * R, xc, yc), "blocks of x and dx", yc);
+        if (yc != xc && yc < S) expect(meet, bwd(cols, yc, 2 * S * R, xc), "blocks of dy and dx", yc);
+      }
+  expect(false, bwd(64, 0, 64, 128), "three blocks", 0);
+  expect(false, bwd(64, 0, 64, 0), "three blocks, in place", 0);
+  expect(true, ln(64, 0, 100, S + 8, nullptr, nullptr), "other strides", 0);
+  // vectors within a row's gap, over its end, over the next row's start, longer than the gap
+  expect(false, ln(64, 0, 64, S, base + 2 * 128, nullptr), "weight in the gap", 0);
+  expect(false, ln(64, 0, 64, S, base + 2 * (S - 64), nullptr), "weight at the gap's end", 0);
+  expect(true, ln(64, 0, 64, S, base + 2 * 127, nullptr), "weight over y", 0);
+  expect(false, ln(64, 0, 64, S, base + 2 * (S - 63), nullptr), "weight over x: both are read", 0);
+  expect(true, ln(64, 64, 0, S, base + 2 * (S - 63), nullptr), "weight over the next row of y", 0);
+  expect(false, ln(64, 0, 64, S, nullptr, base + 2 * 128), "mean in the gap", 0);
+  expect(true, ln(64, 0, 64, S, nullptr, base + 2 * (S - 8)), "mean over x", 0);
+}
+
 // Every operator in every sequence of launches.
 struct Call {
   const char* name;
@@ -328,6 +374,7 @@ int main(int argc, char** argv) {
   if (what == "sort") sort();
   else if (what == "columns") columns();
   else if (what == "scalars") scalars();
+  else if (what == "blocks") blocks();
   else if (what == "failed") failed();
   else if (what == "stale") stale();
   else ++failures;

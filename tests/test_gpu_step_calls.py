@@ -1,5 +1,5 @@
 """Calls of the training-step operators as a program makes them: lists that live only as long as the call,
-sizes beyond one launch, outputs that autograd has saved."""
+sizes beyond one launch, outputs that autograd has saved, blocks of one buffer."""
 import weakref
 
 import pytest
@@ -198,3 +198,32 @@ def test_outputs_of_inference_mode(gpu_available):
         kept = _calls()
     for call, _, _ in kept:  # used outside it
         call()
+
+
+# ------------------------------------------------------------------------------------------------
+# Blocks of columns of one buffer
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=str)
+@pytest.mark.parametrize("rows,cols", [(2, 1), (3, 5), (70, 64), (40, 333), (3000, 1024), (9, 5001), (20, 40001)])
+def test_blocks_of_one_buffer(gpu_available, rows, cols, dtype):
+    """Inputs and outputs side by side in one buffer: the same bits as apart, and nothing beside them."""
+    say("blocks", rows, cols, dtype)
+    x, dy = normal((rows, cols), dtype, 1), normal((rows, cols), dtype, 2)
+    w = normal((cols,), dtype, 3)
+    y, mean, rstd = layer_norm(x, w)
+    want = layer_norm_bwd(dy, x, w, mean, rstd)
+    buf = torch.full((rows, 4 * cols + 3), float("nan"), dtype=dtype, device="cuda")
+    xb, yb, db, gb = (buf[:, i * cols + max(0, i - 1):][:, :cols] for i in range(4))
+    xb.copy_(x)
+    db.copy_(dy)
+    assert torch.equal(layer_norm(xb, w, out=yb)[0], y)
+    got = layer_norm_bwd(db, xb, w, mean, rstd, dx=gb)
+    assert all(map(torch.equal, got, want))
+    for block, value in ((xb, x), (yb, y), (db, dy), (gb, want[0])):
+        assert torch.equal(block, value)
+    assert bool(buf[:, [2 * cols, 3 * cols + 1, 4 * cols + 2]].isnan().all())
+    assert layer_norm_bwd(db, xb, w, mean, rstd, dx=db)[0] is db and torch.equal(db, want[0])
+    if cols > 1:
+        with pytest.raises(TideError):
+            layer_norm(xb, w, out=buf[:, cols - 1:2 * cols - 1])
