@@ -241,8 +241,10 @@ void one_value(const Device& d, Opt t, const char* name, at::ScalarType type) {
   NEED(t->scalar_type() == type, name, " must be of ", c10::toString(type), ", got ", c10::toString(t->scalar_type()));
   NEED(t->numel() == 1, name, " must hold one value");
 }
-// The first of a list tells a tensor of the host apart before the device is asked for.
+// The first of a list, or a matrix of which each row is one, tells a tensor of the host apart before the
+// device is asked for.
 void first_on_gpu(PyObject* list, const char* name) {
+  if (THPVariable_Check(list)) return on_gpu(THPVariable_Unpack(list), name);
   if (PySequence_Check(list) && PySequence_Size(list) > 0)
     if (PyObject* o = PySequence_GetItem(list, 0)) {
       const bool host = THPVariable_Check(o) && !THPVariable_Unpack(o).is_cuda();

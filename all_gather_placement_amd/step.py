@@ -106,7 +106,11 @@ def _call(name, stream, *args):
 
 
 def _init(grads):
-    if not grads:  # no tensor tells that the device is in use
+    try:
+        none = len(grads) == 0
+    except TypeError:  # an iterator
+        none = True
+    if none:  # no tensor tells that the device is in use
         import torch
 
         torch.cuda.init()
@@ -117,9 +121,9 @@ def _init(grads):
 # ------------------------------------------------------------------------------------------------
 
 def grad_norm(grads, norm=None, sumsq=None, workspace=None, stream=None):
-    """L2 norm over a list of contiguous bf16 or fp32 tensors, as an fp32 tensor of one value (`norm`
-    if given).  `sumsq`, an fp64 tensor of one value, also receives the sum of squares: a data-parallel
-    job all-reduces it and clips by :func:`grad_clip`."""
+    """L2 norm over a list (or other iterable) of contiguous bf16 or fp32 tensors, as an fp32 tensor of one
+    value (`norm` if given).  `sumsq`, an fp64 tensor of one value, also receives the sum of squares: a
+    data-parallel job all-reduces it and clips by :func:`grad_clip`."""
     _init(grads)
     if stream is None:
         return (_step or load_step_binding()).grad_norm(grads, norm, sumsq, workspace)

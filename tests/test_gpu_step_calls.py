@@ -90,6 +90,18 @@ def test_generators_give_what_lists_give(gpu_available, dtype):
     assert torch.equal(grad_norm(tuple(g * 0.5 for g in grads)), want)
 
 
+def test_a_matrix_is_a_list_of_its_rows(gpu_available):
+    m = normal((7, 501), FP32, 1)
+    want = grad_norm(list(m))
+    assert torch.equal(grad_norm(m), want)
+    got = m.clone()
+    assert torch.equal(clip_grad_norm(got, 1.0), want)
+    rows = [r.clone() for r in m]
+    clip_grad_norm(rows, 1.0)
+    assert torch.equal(got, torch.stack(rows))
+    assert float(grad_norm(m[:0])) == 0.0 and float(grad_norm(iter(()))) == 0.0
+
+
 # ------------------------------------------------------------------------------------------------
 # Sizes beyond one launch
 # ------------------------------------------------------------------------------------------------
