@@ -111,6 +111,7 @@ void on_gpu(const at::Tensor& t, const char* name) {
 void on(const Device& d, const at::Tensor& t, const char* name) {
   NEED(t.is_cuda() && t.get_device() == d.index, name, " must be on the current device (cuda:", d.index, "), got ",
        t.device().str());
+  NEED(!t.is_neg(), name, " must not be a negated view: its memory holds the values of the other sign");
 }
 void like(const Device& d, const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape) {
   on(d, t, name);

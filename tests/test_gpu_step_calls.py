@@ -212,6 +212,20 @@ def test_outputs_of_inference_mode(gpu_available):
         call()
 
 
+def test_negated_views_are_refused(gpu_available):
+    """The imaginary part of a conjugate is a view whose memory holds the values of the other sign."""
+    z = torch.complex(normal((5, 1), FP32, 1), normal((5, 1), FP32, 2))
+    x = z.conj().imag
+    assert x.is_neg()
+    dense = x.resolve_neg()
+    ids = torch.tensor([0, 4], device="cuda")
+    for call in (lambda x: layer_norm(x), lambda x: grad_norm([x[0]]), lambda x: clip_grad_norm([x[0]], 1.0),
+                 lambda x: embedding(ids[:1], x[:1]), lambda x: embedding_bwd(ids[:1], x[:1], 3)):
+        with pytest.raises(ValueError, match="negated view"):
+            call(x)
+        call(dense)
+
+
 # ------------------------------------------------------------------------------------------------
 # Blocks of columns of one buffer
 # ------------------------------------------------------------------------------------------------
