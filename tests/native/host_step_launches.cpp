@@ -5,6 +5,7 @@
 //   host_step_launches columns  layer norm and its gradient up to the widest row that is accepted
 //   host_step_launches scalars  norm, sum of squares and workspace over a gradient, an output or each other
 //   host_step_launches blocks   blocks of columns of one buffer, as inputs and outputs
+//   host_step_launches parts    the parts of the table gradient's workspace
 //   host_step_launches failed   no kernel follows one that was not launched
 //   host_step_launches stale    an error of another library's earlier call is neither reported nor cleared
 #include <hip/hip_runtime_api.h>
@@ -291,6 +292,49 @@ static void blocks() {
   expect(true, ln(64, 0, 64, S, nullptr, base + 2 * (S - 8)), "mean over x", 0);
 }
 
+// The workspace's parts lie one behind the other within the bytes that are asked for.
+static int64_t workspace_bytes;
+static int looked_at;
+static void check_parts(const Launch& l, void** args) {
+  if (!l.is("embedding_sort") && !l.is("embedding_sum") && !l.is("embedding_join")) return;
+  ++looked_at;
+  const auto& a = *static_cast<const tide_step::EmbeddingBwdArgs*>(args[0]);
+  const int64_t pieces = (a.tokens + tide_step::kPiece - 1) / tide_step::kPiece;
+  struct Part {
+    const void* p;
+    int64_t bytes, align;
+  };
+  const Part parts[] = {{a.num_sorted, 3 * 4, 4},
+                        {a.sorted_token, a.tokens * 4, 4},
+                        {a.sorted_row, a.tokens * 4, 4},
+                        {a.last_piece, pieces * 4, 4},
+                        {a.runs, pieces * int64_t(sizeof(tide_step::EmbeddingRun)), 4},
+                        {a.partial, pieces * 2 * a.dim * 4, 16}};
+  uintptr_t end = reinterpret_cast<uintptr_t>(at(4));
+  for (const Part& p : parts) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p.p);
+    CHECK(lo >= end && lo % uintptr_t(p.align) == 0, "part %d of %lld tokens of %lld", int(&p - parts), (long long)a.tokens,
+          (long long)a.dim);
+    end = lo + uintptr_t(p.bytes);
+  }
+  CHECK(end <= reinterpret_cast<uintptr_t>(at(4)) + uintptr_t(workspace_bytes), "%lld tokens of %lld", (long long)a.tokens,
+        (long long)a.dim);
+}
+
+static void parts() {
+  for (int64_t tokens : {513, 1025, 1056, 1057, 99999, 1 << 24})
+    for (int64_t dim : {1, 3, 8, 1001, 4096})
+      for (int64_t vocab : {int64_t(1), int64_t(20011), int64_t(1) << 30}) {
+        workspace_bytes = tide_embedding_bwd_workspace(tokens, vocab, dim);
+        on_launch = check_parts;
+        launches.clear();
+        CHECK(tide_embedding_bwd(tokens, at(1), TIDE_INT64, vocab, dim, at(2), TIDE_FP32, 1.0f, 0, at(3), at(4),
+                                 workspace_bytes, nullptr) == TIDE_OK, "%s", describe().c_str());
+        on_launch = nullptr;
+      }
+  CHECK(looked_at > 100, "%d", looked_at);
+}
+
 // Every operator in every sequence of launches.
 struct Call {
   const char* name;
@@ -375,6 +419,7 @@ int main(int argc, char** argv) {
   else if (what == "columns") columns();
   else if (what == "scalars") scalars();
   else if (what == "blocks") blocks();
+  else if (what == "parts") parts();
   else if (what == "failed") failed();
   else if (what == "stale") stale();
   else ++failures;
