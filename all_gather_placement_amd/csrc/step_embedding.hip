@@ -587,8 +587,9 @@ constexpr int64_t kZeroBesideSort = int64_t(256) << 20;
 
 // Up to 1024 tokens are not sorted, 512 where rows are wide: 500 tokens of a text, 512 columns of bf16, 7 us
 // instead of 20, 4096 columns 45 instead of 55; 1000 tokens 10 instead of 22, 4096 columns 57 and 57.  One
-// workgroup sums all tokens of a row, so a long run of a wide row takes longer (500 of 4096 columns 105 us
-// instead of 25): tables of few such rows are left to the sort.
+// workgroup sums all tokens of a row, so a long run of a wide row takes longer (500 of 4096 columns 85 us
+// instead of 18).  How long runs are is known on the device only: tables so small that some row has more than
+// 32 tokens are left to the sort, one frequent id in a larger table is not noticed.
 inline bool sum_directly(int64_t tokens, int64_t vocab, int64_t vecs) {
   if (vecs <= 64) return tokens <= 1024;
   return tokens <= (vecs <= 256 ? 1024 : 512) && tokens <= 32 * vocab;

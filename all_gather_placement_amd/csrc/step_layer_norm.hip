@@ -188,7 +188,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_rows_kernel(LayerNo
   }
 }
 
-// Rows wider than the registers: three passes over the row, the later ones from the caches.
+// Rows wider than the registers: three passes over the row, the later ones from the caches (4096 x 40960
+// bf16 196 us, 3.4 TB/s of the bytes that have to move; rows in registers reach 5.9).
 constexpr int kWideThreads = 1024;
 
 template <typename T, typename PT>
@@ -495,7 +496,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void layer_norm_bwd_few_kernel(Laye
   }
 }
 
-// Rows wider than the registers: the input's gradient, two passes over a row.
+// Rows wider than the registers: the input's gradient, two passes over a row (4096 x 40960 bf16 370 us with
+// the sums below, a third pass; 2.7 TB/s of the bytes that have to move).
 template <typename T, typename PT>
 __global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_wide_kernel(LayerNormBwdArgs a) {
   __shared__ float lds[2][2][16];
@@ -621,7 +623,11 @@ void with_lanes(int64_t vecs, F&& f) {
 // Forward: three vectors a lane and two rows a workgroup keep about 16 waves with 60 KiB of loads in
 // flight on a compute unit and halve the reads of weight and bias (32760 x 5120 bf16: 113 us; two
 // vectors 122, four 119, one row 122, ten vectors in one wave, without a barrier, 146; a copy of the same
-// bytes takes 109).  Few rows go to as many waves as they fill: the time is one row's.
+// bytes takes 109).  Two vectors where they leave fewer lanes of the first waves empty (600 MB of bf16: 96
+// vectors 112 us, with three 122; 224 vectors 107 and 117; but 160 vectors 119 and 107).  Of 1024 vectors two
+// (109 us, with three 119) and of 2048 four (116 and 155) would be faster; they are not told apart.
+// Few rows go to as many waves as they fill: the time is one row's (1024 rows of 1024 vectors 10.8 us, with
+// three vectors and two rows 11.3; at 2048 rows both 17.2).
 template <typename F>
 bool with_rows(int64_t vecs, int64_t rows, F&& f) {
   const auto waves = [&](int nv) { return int(ceil_div(vecs, 64 * nv)); };
@@ -633,9 +639,14 @@ bool with_rows(int64_t vecs, int64_t rows, F&& f) {
   else f(Int<3>(), Int<1>(), waves(3));
   return true;
 }
-// Backward: the sums down the columns take 16 registers for a vector of bf16, so a lane holds at most
-// two; beyond, rows are streamed.  Sixteen waves are resident on a compute unit (8192 x 8192 bf16, two
+// Backward: the sums down the columns take 16 registers for a vector of bf16 (of fp32 eight, held to the same
+// limit), so a lane holds at most two; beyond, rows are streamed.  Two vectors of two rows do not fit (38400 x
+// 4096 bf16 598 us instead of 159).  Sixteen waves are resident on a compute unit (8192 x 8192 bf16, two
 // vectors, 512 workgroups of 8 waves: 72 us, with the partial sums 6.1 TB/s; 16 waves of one vector 79).
+// From two waves' width on, up to eight, one vector of two rows is faster (with the join, bf16: 4096 rows of 192
+// vectors 18 us, two vectors of one row 24; 38400 of 512 159 and 178); beyond, and in rows of one wave, where
+// many rows count, two vectors of one row (19200 of 1024 162 us and 169; 153600 of 128 168 and 180, but 4096 of
+// 128 22 and 17).
 template <typename F>
 bool with_bwd_rows(int64_t vecs, F&& f) {
   const auto waves = [&](int nv) { return int(ceil_div(vecs, 64 * nv)); };

@@ -3,6 +3,7 @@
 //
 //   host_step_launches sort     table gradients up to the largest vocabulary that is accepted
 //   host_step_launches columns  layer norm and its gradient up to the widest row that is accepted
+//   host_step_launches far      lookups and norms up to the largest sizes that are accepted
 //   host_step_launches scalars  norm, sum of squares and workspace over a gradient, an output or each other
 //   host_step_launches blocks   blocks of columns of one buffer, as inputs and outputs
 //   host_step_launches parts    the parts of the table gradient's workspace
@@ -170,6 +171,29 @@ static void columns() {
         CHECK(layer_norm_bwd(rows, cols, false, dtype) == TIDE_OK, "%lld x %lld: %s", (long long)rows, (long long)cols,
               describe().c_str());
       }
+}
+
+static void far() {
+  const int64_t most = (int64_t(1) << 31) - 1;
+  for (int64_t tokens : {int64_t(1), most})
+    for (int64_t dim : {int64_t(1), int64_t(9), int64_t(512), int64_t(8191), most})
+      for (int ids : {TIDE_INT32, TIDE_INT64}) {
+        if (tokens > (int64_t(1) << 44) / dim) continue;
+        launches.clear();
+        CHECK(tide_embedding(tokens, at(1), ids, 100, dim, at(2), TIDE_BF16, 1.0f, at(3), nullptr) == TIDE_OK, "%lld x %lld: %s",
+              (long long)tokens, (long long)dim, describe().c_str());
+        launches.clear();
+        CHECK(tide_embedding_bwd(tokens, at(1), ids, 100, dim, at(2), TIDE_BF16, 1.0f, 0, at(3), at(4), kWorkspace,
+                                 nullptr) == TIDE_OK, "%lld x %lld: %s", (long long)tokens, (long long)dim, describe().c_str());
+      }
+  const int64_t numel = int64_t(1) << 42;
+  const void* grad = at(1);
+  void* out = at(1);
+  for (int dtype : {TIDE_BF16, TIDE_FP32}) {
+    launches.clear();
+    CHECK(tide_clip_grad_norm(1, &grad, &out, &numel, dtype, 1.0, static_cast<double*>(at(2)), static_cast<float*>(at(3)),
+                              at(4), kWorkspace, nullptr) == TIDE_OK, "%s", describe().c_str());
+  }
 }
 
 // Refused before anything is launched, or not at all.
@@ -417,6 +441,7 @@ int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "sort") sort();
   else if (what == "columns") columns();
+  else if (what == "far") far();
   else if (what == "scalars") scalars();
   else if (what == "blocks") blocks();
   else if (what == "parts") parts();

@@ -23,7 +23,7 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("what", ["sort", "columns", "scalars", "blocks", "parts", "failed", "stale"])
+@pytest.mark.parametrize("what", ["sort", "columns", "far", "scalars", "blocks", "parts", "failed", "stale"])
 def test_launches(program, what):
     res = subprocess.run([program, what], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0 and "0 failures" in res.stdout, res.stdout + res.stderr[-4000:]
