@@ -5,19 +5,30 @@ marshals arguments to it.  Importing the package does not load the library; the 
 and fails loudly if it has not been built (``python -m all_gather_placement_amd.build``).
 
 ``libtide_step.so`` holds the training-step operators on either side of the collectives (gradient norm
-and clipping, layer norm, embedding, with their gradients); they are bound in :mod:`.step` and its
-compiled module ``_step.so``.
+and clipping, layer norm, embedding, tokens sorted by expert and back, rotary positions, dropout, with
+their gradients); they are bound in :mod:`.step` and its compiled module ``_step.so``.
 """
 from .step import (  # noqa: F401
+    ExpertSort,
     clip_grad_norm,
+    dropout,
+    dropout_bwd,
     embedding,
     embedding_bwd,
+    expert_combine,
+    expert_combine_bwd,
+    expert_dispatch,
+    expert_dispatch_bwd,
+    expert_sort,
     grad_clip,
     grad_norm,
     layer_norm,
     layer_norm_bwd,
     load_step_binding,
     load_step_library,
+    rotary,
+    rotary_bwd,
+    rotary_freqs,
     step_library_path,
 )
 from .tide import (  # noqa: F401

@@ -34,7 +34,8 @@ SOURCES = ["layout.cpp", "api.cpp", "kernels.hip"]
 PROBE_LIB = os.path.join(PKG, "libtide_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 STEP_LIB = os.path.join(PKG, "libtide_step.so")
-STEP_SOURCES = ["step_api.cpp", "step_norm.hip", "step_layer_norm.hip", "step_embedding.hip"]
+STEP_SOURCES = ["step_api.cpp", "step_block_api.cpp", "step_norm.hip", "step_layer_norm.hip", "step_embedding.hip",
+                "step_experts.hip", "step_rotary.hip", "step_dropout.hip"]
 STEP_BINDING = os.path.join(PKG, "_step.so")
 STEP_BINDING_SOURCES = ["step_binding.cpp"]
 ARCH = "gfx950"
@@ -45,7 +46,7 @@ HASHED = {
          + [os.path.join(INCLUDE, "tide.h")],
     PROBE_LIB: [os.path.join(CSRC, f) for f in ("probe.hip", "tide_internal.h")]
                + [os.path.join(INCLUDE, "tide_probe.h")],
-    STEP_LIB: [os.path.join(CSRC, f) for f in (*STEP_SOURCES, "step_internal.h", "step_device.h")]
+    STEP_LIB: [os.path.join(CSRC, f) for f in (*STEP_SOURCES, "step_internal.h", "step_checks.h", "step_device.h", "step_grid.h")]
               + [os.path.join(INCLUDE, f) for f in ("tide_step.h", "tide.h")],
     STEP_BINDING: [os.path.join(CSRC, f) for f in STEP_BINDING_SOURCES]
                   + [os.path.join(INCLUDE, f) for f in ("tide_step.h", "tide.h")],

@@ -167,11 +167,13 @@ struct Output {
     return given;
   }
 };
-PyObject* triple(const Output& a, const Output& b, const Output& c) {
-  PyObject* r = PyTuple_New(3);
+template <typename... Outputs>
+PyObject* together(const Outputs&... outputs) {
+  const Output* o[] = {&outputs...};
+  constexpr int kCount = int(sizeof...(Outputs));
+  PyObject* r = PyTuple_New(kCount);
   if (r == nullptr) return nullptr;
-  const Output* o[] = {&a, &b, &c};
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < kCount; ++i) {
     PyObject* x = o[i]->result();
     if (x == nullptr) {
       Py_DECREF(r);
@@ -388,7 +390,7 @@ PyObject* layer_norm(Args a, Py_ssize_t n) {
                         code(params.type), float(number(a[3])), y.t->data_ptr(), Matrix(*y.t, "out").stride,
                         static_cast<float*>(mean.t->data_ptr()), static_cast<float*>(rstd.t->data_ptr()), d.stream()),
         "tide_layer_norm");
-  return triple(y, mean, rstd);
+  return together(y, mean, rstd);
 }
 
 // dy, x, weight, mean, rstd, dx, dweight, dbias, workspace
@@ -423,7 +425,7 @@ PyObject* layer_norm_bwd(Args a, Py_ssize_t n) {
                             static_cast<float*>(rstd.data_ptr()), dx.t->data_ptr(), Matrix(*dx.t, "dx").stride,
                             dw.t->data_ptr(), db.t->data_ptr(), ws.p, ws.bytes, d.stream()),
         "tide_layer_norm_bwd");
-  return triple(dx, dw, db);
+  return together(dx, dw, db);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -486,6 +488,275 @@ PyObject* embedding_bwd(Args a, Py_ssize_t n) {
   return out.result();
 }
 
+// ---------------------------------------------------------------------------------------------
+// Experts
+// ---------------------------------------------------------------------------------------------
+
+// experts, num_experts, align, place, source, offsets, workspace
+PyObject* expert_sort(Args a, Py_ssize_t n) {
+  arity(n, 7);
+  const at::Tensor& ids = tensor(a[0], "experts");
+  on_gpu(ids, "experts");
+  const int64_t experts = whole(a[1]), align = whole(a[2]);
+  NEED(experts >= 1 && experts <= TIDE_MAX_EXPERTS, "num_experts must be from 1 to ", TIDE_MAX_EXPERTS, ", got ", experts);
+  NEED(align >= 1 && align <= INT32_MAX, "align must be at least one, got ", align);
+  const Device d;
+  on(d, ids, "experts");
+  NEED(is_id(ids.scalar_type()), "experts must be of torch.int32 or torch.int64, got ", c10::toString(ids.scalar_type()));
+  dense(ids, "experts");
+  NEED(ids.dim() >= 1 && ids.size(-1) >= 1 && ids.size(-1) <= TIDE_MAX_CHOICES,
+       "experts must be [..., choices] with 1 to ", TIDE_MAX_CHOICES, " choices, got ", ids.sizes());
+  const int32_t choices = int32_t(ids.size(-1));
+  const int64_t tokens = ids.numel() / choices;
+  const int64_t rows = tide_expert_rows(tokens, choices, int32_t(experts), int32_t(align));
+  NEED(rows >= 0, "there must be fewer than 2^31 pairs and rows");
+  const Output place(a[3], "place", [&] { return d.empty(ids.sizes(), at::kInt); });
+  const Output source(a[4], "source", [&] { return d.empty({rows}, at::kInt); });
+  const Output offsets(a[5], "offsets", [&] { return d.empty({experts + 1}, at::kInt); });
+  like(d, *place.t, "place", at::kInt, ids.sizes());
+  like(d, *source.t, "source", at::kInt, {source.t->numel()});
+  NEED(source.t->numel() >= rows, "source must hold ", rows, " rows at least, got ", source.t->numel());
+  like(d, *offsets.t, "offsets", at::kInt, {experts + 1});
+  dense(*place.t, "place");
+  dense(*source.t, "source");
+  dense(*offsets.t, "offsets");
+  const Workspace ws(d, optional(a[6], "workspace"), tide_expert_sort_workspace(tokens, choices, int32_t(experts)),
+                     "tide_expert_sort");
+  check(tide_expert_sort(tokens, choices, ids.data_ptr(), code(ids.scalar_type()), int32_t(experts), int32_t(align),
+                         static_cast<int32_t*>(place.t->data_ptr()), static_cast<int32_t*>(source.t->data_ptr()),
+                         source.t->numel(), static_cast<int32_t*>(offsets.t->data_ptr()), ws.p, ws.bytes, d.stream()),
+        "tide_expert_sort");
+  return together(place, source, offsets);
+}
+
+// place and source, the first two of what expert_sort gives.
+struct Sorted {
+  const at::Tensor *place, *source;
+  int64_t tokens, rows;
+  int32_t choices;
+  Sorted(const Device& d, PyObject* o) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3)
+      refuse(PyExc_TypeError, "sort must be the (place, source, offsets) of expert_sort");
+    place = &tensor(PyTuple_GET_ITEM(o, 0), "place");
+    source = &tensor(PyTuple_GET_ITEM(o, 1), "source");
+    for (const auto& [t, name] : {std::pair(place, "place"), std::pair(source, "source")}) {
+      on(d, *t, name);
+      NEED(t->scalar_type() == at::kInt, name, " must be of Int, got ", c10::toString(t->scalar_type()));
+      dense(*t, name);
+    }
+    NEED(place->dim() >= 1 && place->size(-1) >= 1 && place->size(-1) <= TIDE_MAX_CHOICES,
+         "place must be [..., choices] with 1 to ", TIDE_MAX_CHOICES, " choices, got ", place->sizes());
+    NEED(source->dim() == 1, "source must be [rows], got ", source->sizes());
+    choices = int32_t(place->size(-1));
+    tokens = place->numel() / choices;
+    rows = source->numel();
+  }
+  const int32_t* at() const { return static_cast<const int32_t*>(place->data_ptr()); }
+  const int32_t* from() const { return static_cast<const int32_t*>(source->data_ptr()); }
+  // A tensor with a vector for each token.
+  Matrix by_token(const at::Tensor& t, const char* name) const {
+    const Matrix m(t, name);
+    NEED(t.dim() == place->dim() && t.sizes().slice(0, size_t(t.dim()) - 1) == place->sizes().slice(0, size_t(t.dim()) - 1),
+         name, " must have shape place.shape[:-1] + (dim,), got ", t.sizes(), " with place ", place->sizes());
+    return m;
+  }
+  Matrix by_row(const at::Tensor& t, const char* name) const {
+    const Matrix m(t, name);
+    NEED(t.dim() == 2 && t.size(0) == rows, name, " must have shape [", rows, ", dim], got ", t.sizes());
+    return m;
+  }
+  c10::SmallVector<int64_t, 6> token_shape(int64_t dim) const {
+    c10::SmallVector<int64_t, 6> shape(place->sizes().begin(), place->sizes().end());
+    shape.back() = dim;
+    return shape;
+  }
+  void weights(const Device& d, const at::Tensor& t, const char* name) const {
+    float_on(d, t, name);
+    NEED(t.sizes() == place->sizes(), name, " must have shape ", place->sizes(), ", got ", t.sizes());
+    dense(t, name);
+  }
+};
+
+// x, sort, out
+PyObject* expert_dispatch(Args a, Py_ssize_t n) {
+  arity(n, 3);
+  const at::Tensor& x = tensor(a[0], "x");
+  on_gpu(x, "x");
+  const Device d;
+  float_on(d, x, "x");
+  const Sorted s(d, a[1]);
+  const Matrix m = s.by_token(x, "x");
+  const Output out(a[2], "out", [&] { return d.empty({s.rows, m.cols}, x.scalar_type()); });
+  like(d, *out.t, "out", x.scalar_type(), {s.rows, m.cols});
+  check(tide_expert_dispatch(s.tokens, s.choices, m.cols, x.data_ptr(), m.stride, code(x.scalar_type()), s.at(), s.from(),
+                             s.rows, out.t->data_ptr(), Matrix(*out.t, "out").stride, d.stream()),
+        "tide_expert_dispatch");
+  return out.result();
+}
+
+// rows, weights, sort, out
+PyObject* expert_combine(Args a, Py_ssize_t n) {
+  arity(n, 4);
+  const at::Tensor& rows = tensor(a[0], "rows");
+  on_gpu(rows, "rows");
+  const Device d;
+  float_on(d, rows, "rows");
+  const Sorted s(d, a[2]);
+  const Matrix m = s.by_row(rows, "rows");
+  const Opt weights = optional(a[1], "weights");
+  if (weights != nullptr) s.weights(d, *weights, "weights");
+  const auto shape = s.token_shape(m.cols);
+  const Output out(a[3], "out", [&] { return d.empty(shape, rows.scalar_type()); });
+  like(d, *out.t, "out", rows.scalar_type(), shape);
+  check(tide_expert_combine(s.tokens, s.choices, m.cols, rows.data_ptr(), m.stride, s.rows, code(rows.scalar_type()),
+                            at_of(weights), weights != nullptr ? code(weights->scalar_type()) : TIDE_FP32, s.at(),
+                            out.t->data_ptr(), Matrix(*out.t, "out").stride, d.stream()),
+        "tide_expert_combine");
+  return out.result();
+}
+
+// dy, rows, weights, sort, drows, dweights
+PyObject* expert_combine_bwd(Args a, Py_ssize_t n) {
+  arity(n, 6);
+  const at::Tensor &dy = tensor(a[0], "dy"), &rows = tensor(a[1], "rows"), &weights = tensor(a[2], "weights");
+  on_gpu(dy, "dy");
+  const Device d;
+  float_on(d, rows, "rows");
+  const Sorted s(d, a[3]);
+  const Matrix m = s.by_row(rows, "rows");
+  like(d, dy, "dy", rows.scalar_type(), s.token_shape(m.cols));
+  s.weights(d, weights, "weights");
+  const Output drows(a[4], "drows", [&] { return d.empty(rows.sizes(), rows.scalar_type()); });
+  const Output dweights(a[5], "dweights", [&] { return d.empty(weights.sizes(), weights.scalar_type()); });
+  like(d, *drows.t, "drows", rows.scalar_type(), rows.sizes());
+  like(d, *dweights.t, "dweights", weights.scalar_type(), weights.sizes());
+  dense(*dweights.t, "dweights");
+  check(tide_expert_combine_bwd(s.tokens, s.choices, m.cols, dy.data_ptr(), Matrix(dy, "dy").stride, rows.data_ptr(),
+                                m.stride, s.rows, code(rows.scalar_type()), weights.data_ptr(),
+                                code(weights.scalar_type()), s.at(), s.from(), drows.t->data_ptr(),
+                                Matrix(*drows.t, "drows").stride, dweights.t->data_ptr(), d.stream()),
+        "tide_expert_combine_bwd");
+  return together(drows, dweights);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------------------------
+
+// A tensor as vectors by token and head: [..., heads, dim] contiguous, or [tokens, heads, dim] of any strides
+// but the last.
+struct HeadVectors {
+  int64_t tokens, heads, dim, token, head;
+  HeadVectors(const at::Tensor& t, const char* name) {
+    NEED(t.dim() >= 2, name, " must have shape [..., heads, dim], got ", t.sizes());
+    heads = t.size(-2);
+    dim = t.size(-1);
+    tokens = 1;
+    for (int64_t i = 0; i < t.dim() - 2; ++i) tokens *= t.size(i);
+    token = heads * dim;
+    head = dim;
+    if (t.is_contiguous()) return;
+    NEED(t.dim() == 3 && (t.stride(2) == 1 || dim <= 1), name,
+         " must be contiguous, or [tokens, heads, dim] with contiguous vectors");
+    token = t.stride(0);
+    head = t.stride(1);
+  }
+};
+
+// x, positions, freqs, sections, pairing, inverse, out
+PyObject* rotary(Args a, Py_ssize_t n) {
+  arity(n, 7);
+  const at::Tensor &x = tensor(a[0], "x"), &positions = tensor(a[1], "positions"), &freqs = tensor(a[2], "freqs");
+  on_gpu(x, "x");
+  int32_t sections[TIDE_ROTARY_MAX_AXES];
+  int64_t pairs = 0;
+  int32_t axes = 0;
+  {  // before addresses are taken: whole() may run Python code
+    const Held seq(PySequence_Fast(a[3], "sections must be a sequence of whole numbers"));
+    if (seq.o == nullptr) throw Refused();
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq.o);
+    NEED(count >= 1 && count <= TIDE_ROTARY_MAX_AXES, "there must be 1 to ", TIDE_ROTARY_MAX_AXES, " sections, got ", count);
+    for (; axes < count; ++axes) {
+      const int64_t v = whole(PySequence_Fast_GET_ITEM(seq.o, axes));
+      NEED(v >= 1 && v <= TIDE_ROTARY_MAX_DIM, "each section must have 1 to ", TIDE_ROTARY_MAX_DIM, " pairs, got ", v);
+      sections[axes] = int32_t(v);
+      pairs += v;
+      NEED(axes + 1 == count || PySequence_Fast_GET_SIZE(seq.o) == count, "sections must not change");
+    }
+  }
+  const bool halves = PyUnicode_Check(a[4]) && PyUnicode_CompareWithASCIIString(a[4], "halves") == 0;
+  NEED(halves || (PyUnicode_Check(a[4]) && PyUnicode_CompareWithASCIIString(a[4], "neighbours") == 0),
+       "pairing must be 'halves' or 'neighbours'");
+  const Device d;
+  float_on(d, x, "x");
+  const HeadVectors v(x, "x");
+  NEED(v.dim >= 1 && v.dim <= TIDE_ROTARY_MAX_DIM && 2 * pairs <= v.dim, "sections of ", pairs, " pairs need vectors of ",
+       2 * pairs, " to ", TIDE_ROTARY_MAX_DIM, " elements, got ", v.dim);
+  on(d, positions, "positions");
+  NEED(is_id(positions.scalar_type()) || positions.scalar_type() == at::kFloat,
+       "positions must be of torch.int32, torch.int64 or torch.float32, got ", c10::toString(positions.scalar_type()));
+  NEED(positions.dim() == x.dim() - 1 && positions.size(0) == axes &&
+           positions.sizes().slice(1) == x.sizes().slice(0, size_t(x.dim()) - 2),
+       "positions must have shape (", axes, ",) + x.shape[:-2], got ", positions.sizes());
+  dense(positions, "positions");
+  like(d, freqs, "freqs", at::kDouble, {pairs});
+  dense(freqs, "freqs");
+  const Output out(a[6], "out", [&] { return d.empty(x.sizes(), x.scalar_type()); });
+  like(d, *out.t, "out", x.scalar_type(), x.sizes());
+  const HeadVectors to(*out.t, "out");
+  check(tide_rotary(v.tokens, v.heads, v.dim, x.data_ptr(), v.token, v.head, code(x.scalar_type()), positions.data_ptr(),
+                    code(positions.scalar_type()), axes, sections, static_cast<const double*>(freqs.data_ptr()),
+                    halves ? TIDE_ROTARY_HALVES : TIDE_ROTARY_NEIGHBOURS, a[5] == Py_True, out.t->data_ptr(), to.token,
+                    to.head, d.stream()),
+        "tide_rotary");
+  return out.result();
+}
+
+// ---------------------------------------------------------------------------------------------
+// Dropout
+// ---------------------------------------------------------------------------------------------
+
+// Any 64 bits, as a number with or without a sign.
+uint64_t bits64(PyObject* o) {
+  int over = 0;
+  const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+  if (over > 0) {
+    const unsigned long long u = PyLong_AsUnsignedLongLong(o);
+    if (u != ~0ull || !PyErr_Occurred()) return u;
+    PyErr_Clear();
+  }
+  NEED(over == 0, "seed must fit 64 bits");
+  if (v == -1 && PyErr_Occurred()) throw Refused();
+  return uint64_t(v);
+}
+
+// x, p, seed, offset, residual, out
+PyObject* dropout(Args a, Py_ssize_t n) {
+  arity(n, 6);
+  const at::Tensor& x = tensor(a[0], "x");
+  on_gpu(x, "x");
+  const double p = number(a[1]);  // before addresses are taken: it may run Python code
+  NEED(p >= 0 && p <= 1, "p must be from 0 to 1, got ", p);
+  const Opt there = THPVariable_Check(a[2]) ? &THPVariable_Unpack(a[2]) : nullptr;
+  const uint64_t seed = there != nullptr ? 0 : bits64(a[2]);
+  const int64_t offset = whole(a[3]);
+  NEED(offset >= 0, "offset must not be negative");
+  const Device d;
+  one_value(d, there, "seed", at::kLong);
+  float_on(d, x, "x");
+  const Matrix m(x, "x");
+  const Opt residual = optional(a[4], "residual");
+  if (residual != nullptr) like(d, *residual, "residual", x.scalar_type(), x.sizes());
+  const Output out(a[5], "out", [&] { return d.empty(x.sizes(), x.scalar_type()); });
+  like(d, *out.t, "out", x.scalar_type(), x.sizes());
+  check(tide_dropout(m.rows, m.cols, x.data_ptr(), m.stride, code(x.scalar_type()), p, seed,
+                     static_cast<const int64_t*>(at_of(there)), offset, at_of(residual),
+                     residual != nullptr ? Matrix(*residual, "residual").stride : m.cols, out.t->data_ptr(),
+                     Matrix(*out.t, "out").stride, d.stream()),
+        "tide_dropout");
+  return out.result();
+}
+
 // TideError, raw stream of a device
 PyObject* configure(Args a, Py_ssize_t n) {
   arity(n, 2);
@@ -522,6 +793,12 @@ PyMethodDef kMethods[] = {method<configure>("configure"),
                           method<layer_norm_bwd>("layer_norm_bwd"),
                           method<embedding>("embedding"),
                           method<embedding_bwd>("embedding_bwd"),
+                          method<expert_sort>("expert_sort"),
+                          method<expert_dispatch>("expert_dispatch"),
+                          method<expert_combine>("expert_combine"),
+                          method<expert_combine_bwd>("expert_combine_bwd"),
+                          method<rotary>("rotary"),
+                          method<dropout>("dropout"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

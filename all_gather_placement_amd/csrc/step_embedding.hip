@@ -18,21 +18,13 @@
 // 200 us (zeros 160, sort 8, sums 23, join 6), of 50021 rows of 1001 fp32 in 20011 75 us (sort beside the
 // zeros 20, sums 48 -- 5.1 TB/s, rows at 4-byte boundaries --, join 7).
 #include "step_device.h"
+#include "step_grid.h"
 #include "step_internal.h"
 
 namespace tide_step {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Workgroups for n items, `per` each: a launch holds less than 2^32 threads, so kernels go on to the
-// items a grid further.
-constexpr int64_t kMaxGrid = int64_t(1) << 21;
-__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline unsigned grid_of(int64_t n, int64_t per) {
-  const int64_t g = ceil_div(n, per);
-  return unsigned(g < kMaxGrid ? g : kMaxGrid);
-}
 
 // ---------------------------------------------------------------------------------------------
 // Lookup
@@ -45,11 +37,6 @@ __device__ __forceinline__ void store_scaled(T* out, int n, const Raw<T, E>& r, 
   for (int k = 0; k < E; ++k) f[k] = inside ? r.get(k) * scale : 0.0f;
   store_vec<T, E, true, kWhole>(out, n, f);
 }
-template <int E>
-__device__ __forceinline__ int tail(int64_t n) {
-  return int(n < E ? n : E);
-}
-
 // Rows of 64 vectors and more: a row goes to 1 << wshift waves of a workgroup of four, a lane holding
 // NV vectors at a time.
 template <typename T, typename I, int NV, bool kWhole>
@@ -120,17 +107,6 @@ constexpr int kRowBits = 9;   // of a row's number within its range
 constexpr int kListed = 448;  // tokens of a wave's list (with the counts less than 64 KiB of LDS)
 static_assert((1 << kRowBits) == kSortMaxRows, "a list's entry is a token of the wave's part and a row");
 
-// Inclusive sum over the wave.
-__device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
-  return v;
-}
-
 // Sum over the workgroup before this thread, and the total.  `lds` holds kSortWaves values.
 __device__ __forceinline__ int block_exclusive(int v, int* lds, int* total) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -145,11 +121,6 @@ __device__ __forceinline__ int block_exclusive(int v, int* lds, int* total) {
   __syncthreads();
   *total = all;
   return before + incl - v;
-}
-
-// Lanes of m below this one.
-__device__ __forceinline__ int lanes_before(uint64_t m) {
-  return int(__builtin_amdgcn_mbcnt_hi(unsigned(m >> 32), __builtin_amdgcn_mbcnt_lo(unsigned(m), 0)));
 }
 
 // The lanes whose `row` equals this lane's, of those in `active`.  A range seldom has more than two

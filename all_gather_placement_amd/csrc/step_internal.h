@@ -147,4 +147,85 @@ struct EmbeddingBwdArgs {
 };
 int launch_embedding_bwd(const EmbeddingBwdArgs& a, int dtype, int ids_dtype, void* stream);
 
+// ---------------------------------------------------------------------------------------------
+// Experts
+// ---------------------------------------------------------------------------------------------
+
+// The sort cuts the pairs into parts, one for each workgroup; the first launch counts each part's pairs
+// of every expert, the second places them.
+constexpr int kExpertParts = 128;
+constexpr int kExpertMinPart = 4096;  // pairs: a part has that many at least, so few pairs are one part in one launch
+inline int expert_parts(int64_t pairs) {
+  const int64_t n = (pairs + kExpertMinPart - 1) / kExpertMinPart;
+  return int(n < 1 ? 1 : n < kExpertParts ? n : kExpertParts);
+}
+
+struct ExpertSortArgs {
+  int64_t pairs;
+  const void* ids;
+  int32_t experts, align;
+  int32_t* place;
+  int32_t* source;
+  int64_t rows;
+  int32_t* offsets;
+  int32_t* counts;  // [parts][experts]; none for one part
+};
+int launch_expert_sort(const ExpertSortArgs& a, int ids_dtype, void* stream);
+
+struct ExpertRowsArgs {
+  int64_t tokens, dim, rows;
+  int32_t choices;
+  const int32_t* place;
+  const int32_t* source;
+  const void* x;  // tokens' rows of dispatch, the sorted buffer of the others
+  int64_t x_stride;
+  const void* dy;
+  int64_t dy_stride;
+  const void* weights;
+  void* out;  // the sorted buffer of dispatch and of combine's gradient
+  int64_t out_stride;
+  void* dweights;
+};
+int launch_expert_dispatch(const ExpertRowsArgs& a, int dtype, void* stream);
+int launch_expert_combine(const ExpertRowsArgs& a, int dtype, int weight_dtype, void* stream);
+int launch_expert_combine_bwd(const ExpertRowsArgs& a, int dtype, int weight_dtype, void* stream);
+
+// ---------------------------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------------------------
+
+struct RotaryArgs {
+  int64_t tokens, heads;
+  int32_t dim, pairs, axes;
+  int32_t ends[TIDE_ROTARY_MAX_AXES];  // the pair behind each axis's last
+  const void* x;
+  int64_t x_token, x_head;
+  const void* positions;
+  const double* freqs;
+  float sign;
+  void* out;
+  int64_t out_token, out_head;
+};
+int launch_rotary(const RotaryArgs& a, int dtype, int positions_dtype, int pairing, void* stream);
+
+// ---------------------------------------------------------------------------------------------
+// Dropout
+// ---------------------------------------------------------------------------------------------
+
+struct DropoutArgs {
+  int64_t rows, cols;
+  const void* x;
+  int64_t x_stride;
+  uint32_t threshold;
+  float scale;
+  uint64_t seed;
+  const int64_t* seed_device;
+  int64_t offset;
+  const void* residual;
+  int64_t residual_stride;
+  void* out;
+  int64_t out_stride;
+};
+int launch_dropout(const DropoutArgs& a, int dtype, void* stream);
+
 }  // namespace tide_step

@@ -1,5 +1,6 @@
 """Binding of libtide_step.so (include/tide_step.h): the training-step operators next to the
-collectives -- global gradient norm and clipping, layer norm, embedding, with their gradients.
+collectives -- global gradient norm and clipping, layer norm, embedding, tokens sorted by expert and
+back, rotary positions, dropout, with their gradients.
 
 Tensors are torch tensors on the current HIP device.  Outputs and workspaces may be passed in; those
 that are not are allocated with torch on the stream the call runs on.  Every call only enqueues
@@ -21,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 from .tide import TideError
 
@@ -65,6 +67,14 @@ def load_step_library():
         "tide_embedding": (i32, [i64, vp, i32, i64, i64, vp, i32, f32, vp, vp]),
         "tide_embedding_bwd_workspace": (i64, [i64, i64, i64]),
         "tide_embedding_bwd": (i32, [i64, vp, i32, i64, i64, vp, i32, f32, i32, vp, vp, i64, vp]),
+        "tide_expert_rows": (i64, [i64, i32, i32, i32]),
+        "tide_expert_sort_workspace": (i64, [i64, i32, i32]),
+        "tide_expert_sort": (i32, [i64, i32, vp, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp]),
+        "tide_expert_dispatch": (i32, [i64, i32, i64, vp, i64, i32, vp, vp, i64, vp, i64, vp]),
+        "tide_expert_combine": (i32, [i64, i32, i64, vp, i64, i64, i32, vp, i32, vp, vp, i64, vp]),
+        "tide_expert_combine_bwd": (i32, [i64, i32, i64, vp, i64, vp, i64, i64, i32, vp, i32, vp, vp, vp, i64, vp, vp]),
+        "tide_rotary": (i32, [i64, i64, i64, vp, i64, i64, i32, vp, i32, i32, vp, vp, i32, i32, vp, i64, i64, vp]),
+        "tide_dropout": (i32, [i64, i64, vp, i64, i32, f64, ctypes.c_uint64, vp, i64, vp, i64, vp, i64, vp]),
         "tide_step_last_hip_error": (i32, []),
         "tide_step_build_id": (ctypes.c_char_p, []),
     }
@@ -188,3 +198,120 @@ def embedding_bwd(ids, dy, vocab, scale=1.0, out=None, accumulate=False, workspa
     if stream is None:
         return (_step or load_step_binding()).embedding_bwd(ids, dy, vocab, scale, out, accumulate, workspace)
     return _call("embedding_bwd", stream, ids, dy, vocab, scale, out, accumulate, workspace)
+
+
+# ------------------------------------------------------------------------------------------------
+# Experts of a mixture
+# ------------------------------------------------------------------------------------------------
+
+class ExpertSort(NamedTuple):
+    """(token, choice) pairs in the order of their experts; int32 tensors.
+
+    place    [..., choices]: each pair's row of the sorted buffer, -1 for a pair without an expert
+    source   [rows]: the number token * choices + choice of each row's pair, -1 for a row of no pair
+    offsets  [num_experts + 1]: where each expert's rows start
+    """
+    place: object
+    source: object
+    offsets: object
+
+
+def expert_sort(experts, num_experts, align=1, place=None, source=None, offsets=None, workspace=None, stream=None):
+    """The order of (token, choice) pairs by expert, as an :class:`ExpertSort`.  `experts`: contiguous int32
+    or int64, [..., choices]; ids outside [0, num_experts) -- padded tokens, another rank's experts -- have
+    no row.  Each expert's rows start on a multiple of `align`, and its pairs keep their order.  There are
+    rows for any ids of this shape; a `source` passed in may have more."""
+    if stream is None:
+        return ExpertSort._make((_step or load_step_binding()).expert_sort(experts, num_experts, align, place, source,
+                                                                           offsets, workspace))
+    return ExpertSort._make(_call("expert_sort", stream, experts, num_experts, align, place, source, offsets,
+                                  workspace))
+
+
+def expert_dispatch(x, sort, out=None, stream=None):
+    """The tokens' vectors in the order of `sort`, an :class:`ExpertSort`: [rows, dim], zeros in rows of no
+    pair.  x is [..., dim], bf16 or fp32, contiguous or a matrix whose rows are."""
+    if stream is None:
+        return (_step or load_step_binding()).expert_dispatch(x, sort, out)
+    return _call("expert_dispatch", stream, x, sort, out)
+
+
+def expert_dispatch_bwd(drows, sort, out=None, stream=None):
+    """Gradient of :func:`expert_dispatch` with respect to x: each token's rows of `drows` [rows, dim], added
+    up in fp32 in the order of its choices."""
+    return expert_combine(drows, None, sort, out, stream)
+
+
+def expert_combine(rows, weights, sort, out=None, stream=None):
+    """The sorted buffer's rows [rows, dim] back at their tokens, [..., dim]: the sum over a token's choices
+    of weights * row, in fp32.  `weights` is [..., choices], bf16 or fp32, or None for ones; those of pairs
+    without a row are not used, and a token without rows is zeros."""
+    if stream is None:
+        return (_step or load_step_binding()).expert_combine(rows, weights, sort, out)
+    return _call("expert_combine", stream, rows, weights, sort, out)
+
+
+def expert_combine_bwd(dy, rows, weights, sort, drows=None, dweights=None, stream=None):
+    """Gradients (drows, dweights) of :func:`expert_combine`: weights * dy at each pair's row, zeros in rows
+    of no pair (`drows` may be `rows` itself), and the products of dy with the rows, 0 for pairs without one."""
+    if stream is None:
+        return (_step or load_step_binding()).expert_combine_bwd(dy, rows, weights, sort, drows, dweights)
+    return _call("expert_combine_bwd", stream, dy, rows, weights, sort, drows, dweights)
+
+
+# ------------------------------------------------------------------------------------------------
+# Rotary positions
+# ------------------------------------------------------------------------------------------------
+
+def rotary_freqs(sections, base=10000.0, shared=False, device=None):
+    """Frequencies for :func:`rotary`, fp64 on the current device: with n pairs in an axis's section, pair i
+    of it turns by base ** (-i / n) for each step; with `shared` all sections share one such ramp."""
+    import torch
+
+    counts = [sum(sections)] if shared else list(sections)
+    ramps = [torch.arange(n, dtype=torch.float64) / n for n in counts]
+    return (float(base) ** -torch.cat(ramps)).to(device if device is not None else torch.device("cuda"))
+
+
+def rotary(x, positions, freqs, sections, pairing="halves", out=None, stream=None):
+    """Pairs of a head's elements turned by positions[axis] * freqs[pair], the angle taken in 64 bits.
+
+    x is [..., heads, dim], bf16 or fp32, contiguous, or [tokens, heads, dim] whose vectors are; `out` may be
+    x itself.  positions is [axes, ...] for the tokens, contiguous int32, int64 or fp32 (text: one axis;
+    video: time, height, width); sections tells how many pairs turn with each axis, one after the other;
+    freqs (fp64) has the pairs' frequencies (:func:`rotary_freqs`).  Of P pairs, pair i is elements i and
+    P + i ("halves") or 2 i and 2 i + 1 ("neighbours"); elements from 2 P on are copied."""
+    if stream is None:
+        return (_step or load_step_binding()).rotary(x, positions, freqs, sections, pairing, False, out)
+    return _call("rotary", stream, x, positions, freqs, sections, pairing, False, out)
+
+
+def rotary_bwd(dy, positions, freqs, sections, pairing="halves", out=None, stream=None):
+    """Gradient of :func:`rotary` with respect to x: dy turned back.  `out` may be dy itself."""
+    if stream is None:
+        return (_step or load_step_binding()).rotary(dy, positions, freqs, sections, pairing, True, out)
+    return _call("rotary", stream, dy, positions, freqs, sections, pairing, True, out)
+
+
+# ------------------------------------------------------------------------------------------------
+# Dropout
+# ------------------------------------------------------------------------------------------------
+
+def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
+    """x / (1 - p) where an element is kept and 0 where it is dropped, plus `residual`; x is bf16 or fp32,
+    contiguous or a matrix whose rows are.
+
+    Whether element e of x is dropped depends on `seed` and offset + e alone (Philox4x32-10, 16 bits an
+    element: the probability is p rounded to a multiple of 2 ** -16, and the scale is that probability's), so
+    the mask is never stored: the same seed and offset give it again.  `seed` is a number of 64 bits or an
+    int64 tensor of one value on the device, which a captured call reads at every replay.  `offset` counts
+    elements: parts of a tensor, on one rank or several, are dropped as the whole would be, and calls that
+    share a seed take numbers apart.  `out` may be x or the residual."""
+    if stream is None:
+        return (_step or load_step_binding()).dropout(x, p, seed, offset, residual, out)
+    return _call("dropout", stream, x, p, seed, offset, residual, out)
+
+
+def dropout_bwd(dy, p, seed, offset=0, out=None, stream=None):
+    """Gradient of :func:`dropout` with respect to x (that of the residual is dy); `out` may be dy itself."""
+    return dropout(dy, p, seed, offset, None, out, stream)
