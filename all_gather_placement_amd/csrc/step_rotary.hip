@@ -4,6 +4,10 @@
 //
 // HBM bounds it: every element is read and written once in 16-byte vectors.  A token's angles are the same
 // for all of its heads, so a workgroup makes those of its tokens once, in LDS, and no table is read.
+//
+// A workgroup has one turn: all of a thread's loads, then the angles while they are in flight, then its stores.
+// Loads and stores are counted together and in order, so a thread that went on to further vectors would wait
+// for its stores with every load: 32760 x 40 x 128 bf16 took 343 us that way, and 110 now (6.1 TB/s).
 #include "step_device.h"
 #include "step_grid.h"
 #include "step_internal.h"
@@ -11,7 +15,11 @@
 namespace tide_step {
 namespace {
 
-constexpr int kThreads = 256;
+// Items of a thread: all of its loads are in flight before the angles are made, and none waits for a store.
+template <bool kHalves, bool kWhole>
+constexpr int kItems = (kHalves ? 2 : 4) / (kWhole ? 1 : 2);
+constexpr int kMaxThreads = 512;
+static_assert(TIDE_ROTARY_MAX_DIM <= 4 * kMaxThreads, "a workgroup takes at least one head");
 constexpr int kAngleBytes = 32768;  // of LDS
 
 // Quotients by a number that is known before the launch, of numbers below 2^31.
@@ -25,7 +33,8 @@ struct Divisor {
 };
 
 struct RotaryShape {
-  int32_t tokens;      // of a workgroup at a time
+  int64_t first_token; // of the launch
+  int32_t tokens;      // of a workgroup
   int32_t heads;       // of a workgroup
   int32_t padded;      // pairs of a token in LDS, whole vectors
   int32_t units;       // vectors (halves: pairs of vectors) of a head that are turned
@@ -60,94 +69,137 @@ __device__ __forceinline__ void turn(double angle, float* cos, float* sin) {
   *sin = q & 2 ? -v : v;
 }
 
-template <typename T, typename P, bool kHalves>
-__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryShape g) {
-  constexpr int E = kVec<T>;
-  extern __shared__ float angles[];  // cos [tokens][padded], then sin
-  float* sines = angles + g.tokens * g.padded;
-  const T* x = static_cast<const T*>(a.x);
-  T* out = static_cast<T*>(a.out);
+// A vector, or the two vectors that are turned against each other.
+template <typename T, bool kHalves>
+struct Item {
+  static constexpr int E = kVec<T>;
+  uint32_t t, u;
+  T* to;
+  Raw<T, E> first, second;
+};
+
+// kWhole: the turned elements and the others are of whole vectors.
+template <typename T, typename P, bool kHalves, bool kWhole>
+__global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, RotaryShape g) {
+  constexpr int E = kVec<T>, N = kItems<kHalves, kWhole>;
+  extern __shared__ f32x4 lds[];
+  float* cosines = reinterpret_cast<float*>(lds);  // [tokens][padded]
+  float* sines = cosines + g.tokens * g.padded;
   const int64_t h0 = int64_t(blockIdx.y) * g.heads;
-  const int heads = int(a.heads - h0 < g.heads ? a.heads - h0 : g.heads);
-  for (int64_t t0 = int64_t(blockIdx.x) * g.tokens; t0 < a.tokens; t0 += int64_t(gridDim.x) * g.tokens) {
-    const int tokens = int(a.tokens - t0 < g.tokens ? a.tokens - t0 : g.tokens);
-    for (uint32_t i = threadIdx.x; i < uint32_t(tokens) * g.pairs.d; i += kThreads) {
-      const uint32_t t = g.pairs(i), p = i - t * g.pairs.d;
-      int axis = 0;
-      while (int(p) >= a.ends[axis]) ++axis;
-      const double at = double(static_cast<const P*>(a.positions)[axis * a.tokens + t0 + t]);
-      float c, s;
-      turn(at * a.freqs[p], &c, &s);
-      angles[t * g.padded + p] = c;
-      sines[t * g.padded + p] = s * a.sign;
+  const uint32_t heads = uint32_t(a.heads - h0 < g.heads ? a.heads - h0 : g.heads);
+  const int turned = 2 * a.pairs, plain = a.dim - turned;
+  const int64_t t0 = g.first_token + int64_t(blockIdx.x) * g.tokens;
+  const uint32_t tokens = uint32_t(a.tokens - t0 < g.tokens ? a.tokens - t0 : g.tokens);
+  Item<T, kHalves> item[N];
+  bool there[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t i = threadIdx.x + j * blockDim.x;
+    const uint32_t t = g.per_token(i), rest = i - t * g.per_token.d, h = g.per_head(rest), u = rest - h * g.per_head.d;
+    there[j] = t < tokens && h < heads;
+    item[j].t = t;
+    item[j].u = u;
+    const T* from = static_cast<const T*>(a.x) + (t0 + t) * a.x_token + (h0 + h) * a.x_head;
+    item[j].to = static_cast<T*>(a.out) + (t0 + t) * a.out_token + (h0 + h) * a.out_head;
+    if (!there[j]) continue;
+    if (int(u) >= g.units) {
+      const int c = (int(u) - g.units) * E;
+      item[j].first = load_vec<T, E, true, kWhole>(from + turned + c, tail<E>(plain - c), plain >= E);
+    } else if constexpr (kHalves) {
+      const int c = int(u) * E, n = tail<E>(a.pairs - c);
+      item[j].first = load_vec<T, E, true, kWhole>(from + c, n, a.pairs >= E);
+      item[j].second = load_vec<T, E, true, kWhole>(from + a.pairs + c, n, a.pairs >= E);
+    } else {
+      const int c = int(u) * E;
+      item[j].first = load_vec<T, E, true, kWhole>(from + c, tail<E>(turned - c), turned >= E);
     }
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < uint32_t(tokens) * g.per_token.d; i += kThreads) {
-      const uint32_t t = g.per_token(i), rest = i - t * g.per_token.d, h = g.per_head(rest), u = rest - h * g.per_head.d;
-      if (int(h) >= heads) continue;
-      const T* from = x + (t0 + t) * a.x_token + (h0 + h) * a.x_head;
-      T* to = out + (t0 + t) * a.out_token + (h0 + h) * a.out_head;
-      if (int(u) >= g.units) {  // columns that are not turned
-        const int c = 2 * a.pairs + (int(u) - g.units) * E, n = tail<E>(a.dim - c);
-        const Raw<T, E> v = load_vec<T, E, true, false>(from + c, n, a.dim - 2 * a.pairs >= E);
-        float f[E];
-  #pragma unroll
-        for (int k = 0; k < E; ++k) f[k] = v.get(k);
-        store_vec<T, E, true, false>(to + c, n, f);
-        continue;
-      }
-      if constexpr (kHalves) {
-        const int p = u * E, n = tail<E>(a.pairs - p);
-        const float* c = angles + t * g.padded + p;
-        const float* s = sines + t * g.padded + p;
-        const Raw<T, E> first = load_vec<T, E, true, false>(from + p, n, a.pairs >= E);
-        const Raw<T, E> second = load_vec<T, E, true, false>(from + a.pairs + p, n, a.pairs >= E);
-        float f[E], f2[E];
-  #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          f[k] = first.get(k) * c[k] - second.get(k) * s[k];
-          f2[k] = second.get(k) * c[k] + first.get(k) * s[k];
-        }
-        store_vec<T, E, true, false>(to + p, n, f);
-        store_vec<T, E, true, false>(to + a.pairs + p, n, f2);
-      } else {
-        const int p = u * (E / 2), n = tail<E>(2 * (a.pairs - p));
-        const float* c = angles + t * g.padded + p;
-        const float* s = sines + t * g.padded + p;
-        const Raw<T, E> v = load_vec<T, E, true, false>(from + 2 * p, n, 2 * a.pairs >= E);
-        float f[E];
-  #pragma unroll
-        for (int k = 0; k < E / 2; ++k) {
-          f[2 * k] = v.get(2 * k) * c[k] - v.get(2 * k + 1) * s[k];
-          f[2 * k + 1] = v.get(2 * k + 1) * c[k] + v.get(2 * k) * s[k];
-        }
-        store_vec<T, E, true, false>(to + 2 * p, n, f);
-      }
+  }
+  loads_first();
+  for (uint32_t i = threadIdx.x; i < tokens * g.pairs.d; i += blockDim.x) {
+    const uint32_t t = g.pairs(i), p = i - t * g.pairs.d;
+    int axis = 0;
+    while (int(p) >= a.ends[axis]) ++axis;
+    const double at = double(static_cast<const P*>(a.positions)[axis * a.tokens + t0 + t]);
+    float c, s;
+    turn(at * a.freqs[p], &c, &s);
+    cosines[t * g.padded + p] = c;
+    sines[t * g.padded + p] = s * a.sign;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (!there[j]) continue;
+    const int u = int(item[j].u);
+    if (u >= g.units) {
+      const int c = (u - g.units) * E;
+      float f[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) f[k] = item[j].first.get(k);
+      store_vec<T, E, true, kWhole>(item[j].to + turned + c, tail<E>(plain - c), f);
+      continue;
     }
-    __syncthreads();  // the angles are used until here
+    constexpr int A = kHalves ? E : E / 2;  // angles of an item
+    typedef float Angles __attribute__((ext_vector_type(A)));
+    const int p = u * A;
+    const Angles c = *reinterpret_cast<const Angles*>(cosines + item[j].t * g.padded + p);
+    const Angles s = *reinterpret_cast<const Angles*>(sines + item[j].t * g.padded + p);
+    if constexpr (kHalves) {
+      float f[E], f2[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float x = item[j].first.get(k), y = item[j].second.get(k);
+        f[k] = x * c[k] - y * s[k];
+        f2[k] = y * c[k] + x * s[k];
+      }
+      const int n = tail<E>(a.pairs - p);
+      store_vec<T, E, true, kWhole>(item[j].to + p, n, f);
+      store_vec<T, E, true, kWhole>(item[j].to + a.pairs + p, n, f2);
+    } else {
+      float f[E];
+#pragma unroll
+      for (int k = 0; k < A; ++k) {
+        const float x = item[j].first.get(2 * k), y = item[j].first.get(2 * k + 1);
+        f[2 * k] = x * c[k] - y * s[k];
+        f[2 * k + 1] = y * c[k] + x * s[k];
+      }
+      store_vec<T, E, true, kWhole>(item[j].to + 2 * p, tail<E>(turned - 2 * p), f);
+    }
   }
 }
 
-template <typename T, typename P>
-int rotary(const RotaryArgs& a, int pairing, hipStream_t s) {
-  constexpr int E = kVec<T>;
-  const bool halves = pairing == TIDE_ROTARY_HALVES, in_place = a.x == a.out;
-  const int units = int(halves ? ceil_div(a.pairs, E) : ceil_div(2 * a.pairs, E));
-  const int copied = in_place ? 0 : int(ceil_div(a.dim - 2 * a.pairs, E));
+template <typename T, typename P, bool kHalves, bool kWhole>
+int rotary(const RotaryArgs& a, hipStream_t s) {
+  constexpr int E = kVec<T>, N = kItems<kHalves, kWhole>;
+  const int units = int(kHalves ? ceil_div(a.pairs, E) : ceil_div(2 * a.pairs, E));
+  const int copied = a.x == a.out ? 0 : int(ceil_div(a.dim - 2 * a.pairs, E));
   const int padded = int(ceil_div(a.pairs, E) * E);
-  constexpr int64_t kMaxHeadParts = 65535;
-  const int64_t heads = ceil_div(a.heads, kMaxHeadParts), items = heads * (units + copied);
-  // items of about four a thread; the angles of so many tokens fit LDS
-  int64_t tokens = ceil_div(4 * kThreads, items);
+  // heads of a workgroup, then its tokens: as many as give each of its threads its items
+  const int64_t most = int64_t(kMaxThreads) * N, per_head = units + copied;
+  int64_t heads = most / per_head < a.heads ? most / per_head : a.heads;
+  heads = ceil_div(a.heads, ceil_div(a.heads, heads));
+  int64_t tokens = 256 * N / (heads * per_head);
   const int64_t fit = kAngleBytes / (padded * 8);
   if (tokens > fit) tokens = fit;
   if (tokens > a.tokens) tokens = a.tokens;
-  const RotaryShape g{int32_t(tokens), int32_t(heads), padded, units, Divisor(uint32_t(units + copied)), Divisor(uint32_t(items)),
-                      Divisor(uint32_t(a.pairs))};
-  const dim3 grid(grid_of(a.tokens, tokens), unsigned(ceil_div(a.heads, heads)));
-  const size_t lds = size_t(tokens) * padded * 8;
-  return halves ? launch(rotary_kernel<T, P, true>, grid, kThreads, lds, s, a, g)
-                : launch(rotary_kernel<T, P, false>, grid, kThreads, lds, s, a, g);
+  if (tokens < 1) tokens = 1;
+  RotaryShape g{0, int32_t(tokens), int32_t(heads), padded, units, Divisor(uint32_t(per_head)),
+                      Divisor(uint32_t(heads * per_head)), Divisor(uint32_t(a.pairs))};
+  const int threads = int(ceil_div(ceil_div(tokens * heads * per_head, N), 64) * 64);
+  // workgroups have one turn: more tokens than a launch holds take another
+  int e = 0;
+  for (; g.first_token < a.tokens && e == 0; g.first_token += kMaxGrid * tokens)
+    e = launch(rotary_kernel<T, P, kHalves, kWhole>,
+               dim3(grid_of(a.tokens - g.first_token, tokens), unsigned(ceil_div(a.heads, heads))), threads,
+               size_t(tokens) * padded * 8, s, a, g);
+  return e;
+}
+template <typename T, typename P>
+int rotary(const RotaryArgs& a, int pairing, hipStream_t s) {
+  constexpr int E = kVec<T>;
+  const bool halves = pairing == TIDE_ROTARY_HALVES;
+  const bool whole = (halves ? a.pairs : 2 * a.pairs) % E == 0 && (a.x == a.out || (a.dim - 2 * a.pairs) % E == 0);
+  if (halves) return whole ? rotary<T, P, true, true>(a, s) : rotary<T, P, true, false>(a, s);
+  return whole ? rotary<T, P, false, true>(a, s) : rotary<T, P, false, false>(a, s);
 }
 template <typename T>
 int rotary(const RotaryArgs& a, int positions_dtype, int pairing, hipStream_t s) {

@@ -250,7 +250,7 @@ tide_status tide_expert_combine_bwd(int64_t tokens, int32_t choices, int64_t dim
  * Errors: TIDE_ERR_INVALID (null or misaligned pointer, sizes, strides, unknown dtype, pairing or
  * inverse, overlap), TIDE_ERR_HIP.
  */
-#define TIDE_ROTARY_MAX_DIM 8192
+#define TIDE_ROTARY_MAX_DIM 2048
 #define TIDE_ROTARY_MAX_AXES 8
 enum { TIDE_ROTARY_HALVES = 0, TIDE_ROTARY_NEIGHBOURS = 1 };
 tide_status tide_rotary(int64_t tokens, int64_t heads, int64_t dim, const void* x, int64_t x_token_stride,
