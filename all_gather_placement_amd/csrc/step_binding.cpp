@@ -133,12 +133,12 @@ struct Workspace {
       NEED(given->scalar_type() == at::kByte, "workspace must be of torch.uint8");
       dense(*given, "workspace");
       NEED(given->numel() >= needed, "workspace must hold ", needed, " bytes, got ", given->numel());
-    } else {
+    } else if (needed > 0) {
       own = d.empty({needed}, at::kByte);
       given = &own;
     }
-    p = given->data_ptr();
-    bytes = given->numel();
+    p = at_of(given);
+    bytes = given != nullptr ? given->numel() : 0;
   }
 };
 

@@ -20,7 +20,7 @@ bool experts_ok(int32_t experts) { return experts >= 1 && experts <= TIDE_MAX_EX
 bool numbers_ok(const int32_t* p, int64_t n) { return n == 0 || (p != nullptr && aligned(p, 4)); }
 
 int64_t sort_bytes(int64_t pairs, int32_t experts) {
-  const int parts = expert_parts(pairs);
+  const int parts = expert_parts(pairs, experts);
   return parts > 1 ? (int64_t(parts) * experts * 4 + 15) / 16 * 16 : 0;
 }
 // What the calls on rows have in common: sizes, and both sides' matrices.

@@ -29,8 +29,8 @@ int launch_expert_sort(const ExpertSortArgs& a, int, void*) {
   ++launched;
   CHECK(a.pairs >= 0 && a.pairs < (int64_t(1) << 31) && a.experts >= 1 && a.experts <= TIDE_MAX_EXPERTS && a.align >= 1);
   CHECK(a.rows >= a.pairs && a.rows < (int64_t(1) << 31));
-  CHECK(expert_parts(a.pairs) >= 1 && expert_parts(a.pairs) <= kExpertParts);
-  CHECK(expert_parts(a.pairs) == 1 || a.counts != nullptr);
+  CHECK(expert_parts(a.pairs, a.experts) >= 1 && expert_parts(a.pairs, a.experts) <= kExpertMaxParts);
+  CHECK(expert_parts(a.pairs, a.experts) == 1 || a.counts != nullptr);
   return 0;
 }
 int launch_expert_dispatch(const ExpertRowsArgs& a, int, void*) {
