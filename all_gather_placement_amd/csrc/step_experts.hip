@@ -289,35 +289,51 @@ inline unsigned zeroing_of(const ExpertRowsArgs& a, int64_t vecs) {
   return a.rows > 0 ? grid_of(a.rows, zero_rows_of(vecs) * (kThreads / 64)) : 0;
 }
 
-// Zeros to the rows of no pair, `count` rows a wave at a time.
+// Workgroups that write zeros among those that take tokens, spread evenly.
+struct Mixed {
+  unsigned tokens, zeros;
+  uint64_t step;  // zeros of all, in 2^-32, rounded up
+  Mixed(unsigned t, unsigned z) : tokens(t), zeros(z), step(t + z > 0 ? ((uint64_t(z) << 32) + t + z - 1) / (t + z) : 0) {}
+  // The workgroup's number among those of its kind.
+  __device__ __forceinline__ unsigned number(bool* zero) const {
+    const unsigned before = unsigned(blockIdx.x * step >> 32);
+    *zero = unsigned((blockIdx.x + 1) * step >> 32) != before;
+    return *zero ? before : blockIdx.x - before;
+  }
+};
+
+// Zeros to the rows of no pair, `count` rows a wave at a time, far apart: many of those rows lie together behind the
+// last expert.
 template <typename T, bool kTiny>
 __device__ __forceinline__ void zero_rows(const ExpertRowsArgs& a, int count, unsigned wg, unsigned wgs) {
   constexpr int E = kVec<T>, kWaves = kThreads / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t pairs = a.tokens * a.choices;
   const float zero[E] = {};
-  for (int64_t r0 = (int64_t(wg) * kWaves + wave) * count; r0 < a.rows; r0 += int64_t(wgs) * kWaves * count) {
+  const int64_t apart = int64_t(wgs) * kWaves;
+  for (int64_t r0 = int64_t(wg) * kWaves + wave; r0 < a.rows; r0 += apart * count) {
     bool none = false;
-    if (lane < count && r0 + lane < a.rows) {
-      const int s = a.source[r0 + lane];
+    if (lane < count && r0 + lane * apart < a.rows) {
+      const int s = a.source[r0 + lane * apart];
       none = s < 0 || s >= pairs;
     }
     for (uint64_t todo = __ballot(none); todo != 0; todo &= todo - 1) {
-      T* to = static_cast<T*>(a.out) + (r0 + __ffsll((unsigned long long)todo) - 1) * a.out_stride;
+      T* to = static_cast<T*>(a.out) + (r0 + (__ffsll((unsigned long long)todo) - 1) * apart) * a.out_stride;
       for (int64_t c = int64_t(lane) * E; c < a.dim; c += 64 * E) Columns<T, kTiny>(c, a.dim).template store<false>(to, zero);
     }
   }
 }
 
-// Workgroups below `sending` take tokens, 1 << lshift lanes each, and write them to their rows; the others write
-// zeros.
+// A token to 1 << lshift lanes, which write it to its rows.
 template <typename T, bool kTiny>
-__global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(ExpertRowsArgs a, unsigned sending, int lshift,
+__global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(ExpertRowsArgs a, Mixed mixed, int lshift,
                                                                    int zero_count) {
   constexpr int E = kVec<T>;
-  if (blockIdx.x >= sending) return zero_rows<T, kTiny>(a, zero_count, blockIdx.x - sending, gridDim.x - sending);
+  bool zero;
+  const unsigned wg = mixed.number(&zero);
+  if (zero) return zero_rows<T, kTiny>(a, zero_count, wg, mixed.zeros);
   const Lanes l(lshift);
-  for (int64_t t = int64_t(blockIdx.x) * l.per + l.group; t < a.tokens; t += int64_t(sending) * l.per) {
+  for (int64_t t = int64_t(wg) * l.per + l.group; t < a.tokens; t += int64_t(mixed.tokens) * l.per) {
     const T* from = static_cast<const T*>(a.x) + t * a.x_stride;
     const int32_t* place = a.place + t * a.choices;
     for (int64_t c = int64_t(l.lane) * E; c < a.dim; c += int64_t(E) << lshift) {
@@ -387,13 +403,15 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(ExpertRowsArgs
   }
 }
 
-// Workgroups below `summing` take tokens, the others write zeros.  A token belongs to kLanes lanes; with 64, to
+// A token belongs to kLanes lanes; with 64, to
 // 1 << wshift waves of the workgroup's four, whose sums meet in LDS.
 template <typename T, int N, bool kTiny, int kLanes, int kPast>
 __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRowsArgs a, bool bf16_weights,
-                                                                      unsigned summing, int wshift, int zero_count) {
+                                                                      Mixed mixed, int wshift, int zero_count) {
   constexpr int E = kVec<T>;
-  if (blockIdx.x >= summing) return zero_rows<T, kTiny>(a, zero_count, blockIdx.x - summing, gridDim.x - summing);
+  bool zero;
+  const unsigned wg = mixed.number(&zero);
+  if (zero) return zero_rows<T, kTiny>(a, zero_count, wg, mixed.zeros);
   __shared__ float sums[kThreads / 64][N];
   const int lane = threadIdx.x & (kLanes - 1), per = (kThreads / kLanes) >> wshift;
   int group = threadIdx.x / kLanes;
@@ -405,7 +423,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRows
     else
       static_cast<float*>(a.dweights)[p] = v;
   };
-  for (int64_t t0 = int64_t(blockIdx.x) * per; t0 < a.tokens; t0 += int64_t(summing) * per) {
+  for (int64_t t0 = int64_t(wg) * per; t0 < a.tokens; t0 += int64_t(mixed.tokens) * per) {
     const int64_t t = t0 + (group >> wshift);
     const bool mine = t < a.tokens;
     for (int j0 = 0; j0 < a.choices; j0 += N) {
@@ -484,9 +502,9 @@ int dispatch(const ExpertRowsArgs& a, hipStream_t s) {
   return with_bool(a.dim < kVec<T>, [&](auto tiny) {
     const int64_t vecs = ceil_div(a.dim, kVec<T>);
     const int lshift = lanes_shift(vecs);
-    const unsigned sending = a.tokens > 0 ? grid_of(a.tokens, kThreads >> lshift) : 0;
-    return launch(expert_dispatch_kernel<T, decltype(tiny)::value>, sending + zeroing_of(a, vecs), kThreads, 0, s, a,
-                  sending, lshift, zero_rows_of(vecs));
+    const Mixed mixed(a.tokens > 0 ? grid_of(a.tokens, kThreads >> lshift) : 0, zeroing_of(a, vecs));
+    return launch(expert_dispatch_kernel<T, decltype(tiny)::value>, mixed.tokens + mixed.zeros, kThreads, 0, s, a, mixed,
+                  lshift, zero_rows_of(vecs));
   });
 }
 
@@ -528,10 +546,11 @@ int combine_bwd(const ExpertRowsArgs& a, bool bf16_weights, hipStream_t s) {
   const auto call = [&](auto tiny, auto lanes, auto nt) {
     return with_choices(a.choices, [&](auto n) {
       const int wshift = vecs <= 64 ? 0 : vecs <= 128 ? 1 : 2;
-      const unsigned summing = a.tokens > 0 ? grid_of(a.tokens, (kThreads / decltype(lanes)::value) >> wshift) : 0;
+      const Mixed mixed(a.tokens > 0 ? grid_of(a.tokens, (kThreads / decltype(lanes)::value) >> wshift) : 0,
+                        zeroing_of(a, vecs));
       return launch(expert_combine_bwd_kernel<T, decltype(n)::value, decltype(tiny)::value, decltype(lanes)::value,
                                               decltype(nt)::value>,
-                    summing + zeroing_of(a, vecs), kThreads, 0, s, a, bf16_weights, summing, wshift, zero_rows_of(vecs));
+                    mixed.tokens + mixed.zeros, kThreads, 0, s, a, bf16_weights, mixed, wshift, zero_rows_of(vecs));
     });
   };
   const std::integral_constant<int, 0> plain;
