@@ -7,7 +7,8 @@
 //
 // A workgroup has one turn: all of a thread's loads, then the angles while they are in flight, then its stores.
 // Loads and stores are counted together and in order, so a thread that went on to further vectors would wait
-// for its stores with every load: 32760 x 40 x 128 bf16 took 343 us that way, and 110 now (6.1 TB/s).
+// for its stores with every load: 32760 x 40 x 128 bf16 took 343 us that way, and 108 now (6.2 TB/s).  Heads of
+// few tokens or one head of many are bound by the angles, some 60 instructions each.
 #include "step_device.h"
 #include "step_grid.h"
 #include "step_internal.h"
@@ -18,6 +19,12 @@ namespace {
 // Items of a thread: all of its loads are in flight before the angles are made, and none waits for a store.
 template <bool kHalves, bool kWhole>
 constexpr int kItems = (kHalves ? 2 : 4) / (kWhole ? 1 : 2);
+// A thread has fewer items where it would make more than four angles for them, which all wait for each other (100000
+// tokens of one head of 64 bf16 11.6 us instead of 13.9), and where there would be few workgroups (512 tokens of 32
+// heads of 128 3.6 us instead of 4.1).
+template <typename T, bool kHalves>
+constexpr int kAnglesOf = kHalves ? kVec<T> : kVec<T> / 2;  // of an item
+constexpr int64_t kFewThreads = 512 * 256;
 constexpr int kMaxThreads = 512;
 static_assert(TIDE_ROTARY_MAX_DIM <= 4 * kMaxThreads, "a workgroup takes at least one head");
 constexpr int kAngleBytes = 32768;  // of LDS
@@ -78,8 +85,8 @@ struct Item {
   Raw<T, E> first, second;
 };
 
-// kWhole: the turned elements and the others are of whole vectors.
-template <typename T, typename P, bool kHalves, bool kWhole>
+// kWhole: the turned elements and the others are of whole vectors.  kOnce: they are read past the caches.
+template <typename T, typename P, bool kHalves, bool kWhole, bool kOnce>
 __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, RotaryShape g) {
   constexpr int E = kVec<T>, N = kItems<kHalves, kWhole>;
   extern __shared__ f32x4 lds[];
@@ -104,14 +111,14 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
     if (!there[j]) continue;
     if (int(u) >= g.units) {
       const int c = (int(u) - g.units) * E;
-      item[j].first = load_vec<T, E, true, kWhole>(from + turned + c, tail<E>(plain - c), plain >= E);
+      item[j].first = load_vec<T, E, kOnce, kWhole>(from + turned + c, tail<E>(plain - c), plain >= E);
     } else if constexpr (kHalves) {
       const int c = int(u) * E, n = tail<E>(a.pairs - c);
-      item[j].first = load_vec<T, E, true, kWhole>(from + c, n, a.pairs >= E);
-      item[j].second = load_vec<T, E, true, kWhole>(from + a.pairs + c, n, a.pairs >= E);
+      item[j].first = load_vec<T, E, kOnce, kWhole>(from + c, n, a.pairs >= E);
+      item[j].second = load_vec<T, E, kOnce, kWhole>(from + a.pairs + c, n, a.pairs >= E);
     } else {
       const int c = int(u) * E;
-      item[j].first = load_vec<T, E, true, kWhole>(from + c, tail<E>(turned - c), turned >= E);
+      item[j].first = load_vec<T, E, kOnce, kWhole>(from + c, tail<E>(turned - c), turned >= E);
     }
   }
   loads_first();
@@ -138,7 +145,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
       store_vec<T, E, true, kWhole>(item[j].to + turned + c, tail<E>(plain - c), f);
       continue;
     }
-    constexpr int A = kHalves ? E : E / 2;  // angles of an item
+    constexpr int A = kAnglesOf<T, kHalves>;
     typedef float Angles __attribute__((ext_vector_type(A)));
     const int p = u * A;
     const Angles c = *reinterpret_cast<const Angles*>(cosines + item[j].t * g.padded + p);
@@ -167,7 +174,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
   }
 }
 
-template <typename T, typename P, bool kHalves, bool kWhole>
+template <typename T, typename P, bool kHalves, bool kWhole, bool kOnce>
 int rotary(const RotaryArgs& a, hipStream_t s) {
   constexpr int E = kVec<T>, N = kItems<kHalves, kWhole>;
   const int units = int(kHalves ? ceil_div(a.pairs, E) : ceil_div(2 * a.pairs, E));
@@ -177,29 +184,43 @@ int rotary(const RotaryArgs& a, hipStream_t s) {
   const int64_t most = int64_t(kMaxThreads) * N, per_head = units + copied;
   int64_t heads = most / per_head < a.heads ? most / per_head : a.heads;
   heads = ceil_div(a.heads, ceil_div(a.heads, heads));
-  int64_t tokens = 256 * N / (heads * per_head);
+  int64_t per_thread = N;
+  while (per_thread > 1 && (per_thread * kAnglesOf<T, kHalves> > 4 * heads ||
+                            a.tokens * a.heads * per_head < kFewThreads * per_thread))
+    per_thread /= 2;
+  int64_t tokens = 256 * per_thread / (heads * per_head);
   const int64_t fit = kAngleBytes / (padded * 8);
   if (tokens > fit) tokens = fit;
   if (tokens > a.tokens) tokens = a.tokens;
   if (tokens < 1) tokens = 1;
   RotaryShape g{0, int32_t(tokens), int32_t(heads), padded, units, Divisor(uint32_t(per_head)),
                       Divisor(uint32_t(heads * per_head)), Divisor(uint32_t(a.pairs))};
-  const int threads = int(ceil_div(ceil_div(tokens * heads * per_head, N), 64) * 64);
+  int64_t threads = ceil_div(ceil_div(tokens * heads * per_head, per_thread), 64) * 64;
+  if (threads > kMaxThreads) threads = kMaxThreads;
   // workgroups have one turn: more tokens than a launch holds take another
   int e = 0;
   for (; g.first_token < a.tokens && e == 0; g.first_token += kMaxGrid * tokens)
-    e = launch(rotary_kernel<T, P, kHalves, kWhole>,
-               dim3(grid_of(a.tokens - g.first_token, tokens), unsigned(ceil_div(a.heads, heads))), threads,
+    e = launch(rotary_kernel<T, P, kHalves, kWhole, kOnce>,
+               dim3(grid_of(a.tokens - g.first_token, tokens), unsigned(ceil_div(a.heads, heads))), int(threads),
                size_t(tokens) * padded * 8, s, a, g);
   return e;
 }
+// More than the last-level cache holds, read and written, is read past it: 32760 x 40 x 128 bf16 108 us instead of
+// 112, a seventh of that 17.5 instead of 16.2.  Vectors that end inside others' cache lines need the caches (50000 x 8
+// x 100 with 64 turned 33 us, past them 56).
+constexpr int64_t kPastCaches = int64_t(256) << 20;
+
+template <typename T, typename P, bool kHalves>
+int rotary(const RotaryArgs& a, hipStream_t s) {
+  constexpr int E = kVec<T>;
+  const bool whole = (kHalves ? a.pairs : 2 * a.pairs) % E == 0 && (a.x == a.out || (a.dim - 2 * a.pairs) % E == 0);
+  if (!whole) return rotary<T, P, kHalves, false, false>(a, s);
+  const bool once = 2 * a.tokens * a.heads * a.dim * int64_t(sizeof(T)) > kPastCaches;
+  return once ? rotary<T, P, kHalves, true, true>(a, s) : rotary<T, P, kHalves, true, false>(a, s);
+}
 template <typename T, typename P>
 int rotary(const RotaryArgs& a, int pairing, hipStream_t s) {
-  constexpr int E = kVec<T>;
-  const bool halves = pairing == TIDE_ROTARY_HALVES;
-  const bool whole = (halves ? a.pairs : 2 * a.pairs) % E == 0 && (a.x == a.out || (a.dim - 2 * a.pairs) % E == 0);
-  if (halves) return whole ? rotary<T, P, true, true>(a, s) : rotary<T, P, true, false>(a, s);
-  return whole ? rotary<T, P, false, true>(a, s) : rotary<T, P, false, false>(a, s);
+  return pairing == TIDE_ROTARY_HALVES ? rotary<T, P, true>(a, s) : rotary<T, P, false>(a, s);
 }
 template <typename T>
 int rotary(const RotaryArgs& a, int positions_dtype, int pairing, hipStream_t s) {
