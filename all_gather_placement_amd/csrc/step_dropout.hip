@@ -4,7 +4,7 @@
 //
 // Philox4x32 with 10 rounds makes the bits of eight neighbouring elements from the seed and their number, so
 // no mask is stored or read: HBM bounds it, each element read and written once (32760 x 5120 bf16 with a residual
-// 160 us, 6.3 TB/s).  16 bits an element, not 32: a round's two 64-bit products run at a quarter of the rate of other
+// 158 us, 6.4 TB/s).  16 bits an element, not 32: a round's two 64-bit products run at a quarter of the rate of other
 // integer operations, and at four elements a call they would take as long as the memory does.
 #include "step_device.h"
 #include "step_grid.h"
@@ -123,8 +123,9 @@ __global__ __launch_bounds__(kThreads) void dropout_rows_kernel(DropoutArgs a, i
 }
 
 // More bytes than the last-level cache holds go past the caches where a unit is one vector: 32760 x 5120 bf16 with a
-// residual 160 us instead of 166, a tenth of that 22 instead of 19.5.  The two vectors of a unit of fp32 share cache
-// lines with those of the next lane, which the caches join (half as many rows 167 us, past them 186).
+// residual 158 us instead of 169; an eighth of that, whose inputs the cache may hold, 19.5 instead of 22 where it does.  The
+// two vectors of a unit of fp32 share cache lines with those of the next lane, which the caches join (half as many rows
+// 168 us, past them 187).
 constexpr int64_t kPastCaches = int64_t(256) << 20;
 
 template <typename T, bool kResidual>

@@ -11,8 +11,8 @@
 //
 // The others move rows in 16-byte vectors and are bound by HBM.  A token belongs to one group of lanes, which reads
 // its row once and writes all of its rows of the sorted buffer, or has all of those in flight together: 8192 x 2048
-// bf16 dispatched to eight experts each 61 us (6.0 TB/s; by rows of the sorted buffer, each reading its token's, 77),
-// back 52, the gradients 116 (147 with a wave to a token, which goes on to further columns: loads and stores are
+// bf16 dispatched to eight experts each 62 us (5.9 TB/s; by rows of the sorted buffer, each reading its token's, 77),
+// back 53, the gradients 110 (147 with a wave to a token, which goes on to further columns: loads and stores are
 // counted together and in order, so its later loads wait for its stores).
 #include "step_device.h"
 #include "step_grid.h"
@@ -325,7 +325,7 @@ __device__ __forceinline__ void zero_rows(const ExpertRowsArgs& a, int count, un
 }
 
 // A token to 1 << lshift lanes, which write it to its rows.
-template <typename T, bool kTiny>
+template <typename T, bool kTiny, bool kOnce>
 __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(ExpertRowsArgs a, Mixed mixed, int lshift,
                                                                    int zero_count) {
   constexpr int E = kVec<T>;
@@ -344,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(ExpertRowsArg
       for (int k = 0; k < E; ++k) f[k] = v.get(k);
       for (int j = 0; j < a.choices; ++j) {
         const int row = place[j];
-        if (row >= 0 && row < a.rows) col.template store<false>(static_cast<T*>(a.out) + row * a.out_stride, f);
+        if (row >= 0 && row < a.rows) col.template store<kOnce>(static_cast<T*>(a.out) + row * a.out_stride, f);
       }
     }
   }
@@ -398,14 +398,16 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(ExpertRowsArgs
             for (int k = 0; k < E; ++k) acc[k] = fmaf(ch.w[j], r[j].get(k), acc[k]);
           }
       }
-      col.template store<false>(static_cast<T*>(a.out) + t * a.out_stride, acc);
+      col.template store<kOnce>(static_cast<T*>(a.out) + t * a.out_stride, acc);
     }
   }
 }
 
-// A token belongs to kLanes lanes; with 64, to
-// 1 << wshift waves of the workgroup's four, whose sums meet in LDS.
-template <typename T, int N, bool kTiny, int kLanes, int kPast>
+// A token belongs to kLanes lanes; with 64, to 1 << wshift waves of the workgroup's four, whose sums meet in LDS.  Rows
+// of whole waves are read and written past the caches, beside the zeros, which go through them: 8192 x 2048 bf16 by
+// eight experts 110 us, through the caches 129, a quarter of that 38 and 47; rows of 100 columns 19 us, past the
+// caches 21.
+template <typename T, int N, bool kTiny, int kLanes>
 __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRowsArgs a, bool bf16_weights,
                                                                       Mixed mixed, int wshift, int zero_count) {
   constexpr int E = kVec<T>;
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRows
           Raw<T, E> r[N];
 #pragma unroll
           for (int j = 0; j < N; ++j)
-            if (ch.row[j] >= 0) r[j] = col.template load<(kPast > 0)>(static_cast<const T*>(a.x) + ch.row[j] * a.x_stride);
+            if (ch.row[j] >= 0) r[j] = col.template load<(kLanes == 64)>(static_cast<const T*>(a.x) + ch.row[j] * a.x_stride);
           loads_first();
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRows
               if (kTiny || k >= col.shared) dot[j] = fmaf(d.get(k), r[j].get(k), dot[j]);
               f[k] = ch.w[j] * d.get(k);
             }
-            col.template store<(kPast > 1)>(static_cast<T*>(a.out) + ch.row[j] * a.out_stride, f);
+            col.template store<(kLanes == 64)>(static_cast<T*>(a.out) + ch.row[j] * a.out_stride, f);
           }
           if constexpr (kLanes < 64) break;  // lanes for all of a row
         }
@@ -497,15 +499,23 @@ int with_bool(bool b, F&& f) {
   return b ? f(std::true_type()) : f(std::false_type());
 }
 
+// Zeros are written through the caches, which take them up beside what goes past them: with at least an eighth of the
+// pairs as many rows of no pair, pairs' rows past the caches make the best of both (8192 tokens of 2048 bf16 to eight
+// experts each, a quarter of that of no pair: 62 us instead of 71); without, all go through them (57 us instead of 63).
+// Rows of less than 64 vectors share their ends' cache lines with others (30000 x 100 bf16 to six experts 13 us, past
+// the caches 20).
 template <typename T>
 int dispatch(const ExpertRowsArgs& a, hipStream_t s) {
-  return with_bool(a.dim < kVec<T>, [&](auto tiny) {
-    const int64_t vecs = ceil_div(a.dim, kVec<T>);
+  const int64_t vecs = ceil_div(a.dim, kVec<T>), pairs = a.tokens * a.choices;
+  const auto call = [&](auto tiny, auto once) {
     const int lshift = lanes_shift(vecs);
     const Mixed mixed(a.tokens > 0 ? grid_of(a.tokens, kThreads >> lshift) : 0, zeroing_of(a, vecs));
-    return launch(expert_dispatch_kernel<T, decltype(tiny)::value>, mixed.tokens + mixed.zeros, kThreads, 0, s, a, mixed,
-                  lshift, zero_rows_of(vecs));
-  });
+    return launch(expert_dispatch_kernel<T, decltype(tiny)::value, decltype(once)::value>, mixed.tokens + mixed.zeros,
+                  kThreads, 0, s, a, mixed, lshift, zero_rows_of(vecs));
+  };
+  if (a.dim < kVec<T>) return call(std::true_type(), std::false_type());
+  return with_bool(vecs >= 64 && a.dim % kVec<T> == 0 && a.rows - pairs >= pairs / 8,
+                   [&](auto once) { return call(std::false_type(), once); });
 }
 
 // f(choices in flight) as a constant.
@@ -516,12 +526,10 @@ int with_choices(int choices, F&& f) {
   return f(std::integral_constant<int, 2>());
 }
 
-// A sorted buffer of more bytes is read past the caches, which keep what is written for the next operator: the gradient
-// of 8192 x 2048 bf16 by eight experts (256 MiB) takes 94 us instead of 113, of 5 of 8 KiB of fp32 columns (164 MB) 64
-// instead of 73; a quarter of that, which the caches hold, 35 us instead of 41 the other way.
+// A sorted buffer of more bytes is read past the caches on its way back, and what it gives written past them: 8192
+// tokens of 2048 bf16 by eight experts (256 MiB) 52 us instead of 59, 40000 251 instead of 283; 4099 x 3 rows of 1001 fp32
+// (49 MB) 11.3 us, past the caches 12.2.
 constexpr int64_t kReadOnce = int64_t(128) << 20;
-// Beyond this the gradient is written past them too (1.3 GB 543 us instead of 558; 256 MiB 108 instead of 94).
-constexpr int64_t kWrittenOnce = int64_t(512) << 20;
 template <typename T>
 int64_t bytes_of(const ExpertRowsArgs& a) {
   return a.rows * a.dim * int64_t(sizeof(T));
@@ -543,24 +551,19 @@ int combine(const ExpertRowsArgs& a, bool bf16_weights, hipStream_t s) {
 template <typename T>
 int combine_bwd(const ExpertRowsArgs& a, bool bf16_weights, hipStream_t s) {
   const int64_t vecs = ceil_div(a.dim, kVec<T>);
-  const auto call = [&](auto tiny, auto lanes, auto nt) {
+  const auto call = [&](auto tiny, auto lanes) {
     return with_choices(a.choices, [&](auto n) {
       const int wshift = vecs <= 64 ? 0 : vecs <= 128 ? 1 : 2;
       const Mixed mixed(a.tokens > 0 ? grid_of(a.tokens, (kThreads / decltype(lanes)::value) >> wshift) : 0,
                         zeroing_of(a, vecs));
-      return launch(expert_combine_bwd_kernel<T, decltype(n)::value, decltype(tiny)::value, decltype(lanes)::value,
-                                              decltype(nt)::value>,
+      return launch(expert_combine_bwd_kernel<T, decltype(n)::value, decltype(tiny)::value, decltype(lanes)::value>,
                     mixed.tokens + mixed.zeros, kThreads, 0, s, a, bf16_weights, mixed, wshift, zero_rows_of(vecs));
     });
   };
-  const std::integral_constant<int, 0> plain;
-  if (a.dim < kVec<T>) return call(std::true_type(), std::integral_constant<int, 1>(), plain);
-  if (vecs <= 4) return call(std::false_type(), std::integral_constant<int, 4>(), plain);
-  if (vecs <= 16) return call(std::false_type(), std::integral_constant<int, 16>(), plain);
-  const std::integral_constant<int, 64> wave;
-  if (bytes_of<T>(a) > kWrittenOnce) return call(std::false_type(), wave, std::integral_constant<int, 2>());
-  if (bytes_of<T>(a) > kReadOnce) return call(std::false_type(), wave, std::integral_constant<int, 1>());
-  return call(std::false_type(), wave, plain);
+  if (a.dim < kVec<T>) return call(std::true_type(), std::integral_constant<int, 1>());
+  if (vecs <= 4) return call(std::false_type(), std::integral_constant<int, 4>());
+  if (vecs <= 16) return call(std::false_type(), std::integral_constant<int, 16>());
+  return call(std::false_type(), std::integral_constant<int, 64>());
 }
 
 }  // namespace

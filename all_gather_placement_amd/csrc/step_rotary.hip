@@ -142,7 +142,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
       float f[E];
 #pragma unroll
       for (int k = 0; k < E; ++k) f[k] = item[j].first.get(k);
-      store_vec<T, E, true, kWhole>(item[j].to + turned + c, tail<E>(plain - c), f);
+      store_vec<T, E, kWhole, kWhole>(item[j].to + turned + c, tail<E>(plain - c), f);
       continue;
     }
     constexpr int A = kAnglesOf<T, kHalves>;
@@ -159,8 +159,8 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
         f2[k] = y * c[k] + x * s[k];
       }
       const int n = tail<E>(a.pairs - p);
-      store_vec<T, E, true, kWhole>(item[j].to + p, n, f);
-      store_vec<T, E, true, kWhole>(item[j].to + a.pairs + p, n, f2);
+      store_vec<T, E, kWhole, kWhole>(item[j].to + p, n, f);
+      store_vec<T, E, kWhole, kWhole>(item[j].to + a.pairs + p, n, f2);
     } else {
       float f[E];
 #pragma unroll
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
         f[2 * k] = x * c[k] - y * s[k];
         f[2 * k + 1] = y * c[k] + x * s[k];
       }
-      store_vec<T, E, true, kWhole>(item[j].to + 2 * p, tail<E>(turned - 2 * p), f);
+      store_vec<T, E, kWhole, kWhole>(item[j].to + 2 * p, tail<E>(turned - 2 * p), f);
     }
   }
 }
