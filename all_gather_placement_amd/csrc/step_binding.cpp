@@ -692,6 +692,7 @@ PyObject* rotary(Args a, Py_ssize_t n) {
   const HeadVectors v(x, "x");
   NEED(v.dim >= 1 && v.dim <= TIDE_ROTARY_MAX_DIM && 2 * pairs <= v.dim, "sections of ", pairs, " pairs need vectors of ",
        2 * pairs, " to ", TIDE_ROTARY_MAX_DIM, " elements, got ", v.dim);
+  NEED(v.heads <= TIDE_ROTARY_MAX_HEADS, "x must have at most ", TIDE_ROTARY_MAX_HEADS, " heads, got ", v.heads);
   on(d, positions, "positions");
   NEED(is_id(positions.scalar_type()) || positions.scalar_type() == at::kFloat,
        "positions must be of torch.int32, torch.int64 or torch.float32, got ", c10::toString(positions.scalar_type()));

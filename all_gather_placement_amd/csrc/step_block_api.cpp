@@ -170,7 +170,7 @@ tide_status tide_rotary(int64_t tokens, int64_t heads, int64_t dim, const void* 
                         int64_t x_head_stride, int32_t dtype, const void* positions, int32_t positions_dtype,
                         int32_t axes, const int32_t* sections, const double* freqs, int32_t pairing, int32_t inverse,
                         void* out, int64_t out_token_stride, int64_t out_head_stride, void* stream) {
-  if (tokens < 0 || heads < 0 || tokens >= kInt31 || heads >= kInt31 || dim < 1 || dim > TIDE_ROTARY_MAX_DIM ||
+  if (tokens < 0 || heads < 0 || tokens >= kInt31 || heads > TIDE_ROTARY_MAX_HEADS || dim < 1 || dim > TIDE_ROTARY_MAX_DIM ||
       (tokens > 0 && heads > kMaxElems / dim / tokens) || !float_type(dtype) ||
       (positions_dtype != TIDE_INT32 && positions_dtype != TIDE_INT64 && positions_dtype != TIDE_FP32) || axes < 1 ||
       axes > TIDE_ROTARY_MAX_AXES || sections == nullptr ||

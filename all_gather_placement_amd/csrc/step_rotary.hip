@@ -26,7 +26,7 @@ template <typename T, bool kHalves>
 constexpr int kAnglesOf = kHalves ? kVec<T> : kVec<T> / 2;  // of an item
 constexpr int64_t kFewThreads = 512 * 256;
 constexpr int kMaxThreads = 512;
-static_assert(TIDE_ROTARY_MAX_DIM <= 4 * kMaxThreads, "a workgroup takes at least one head");
+static_assert(TIDE_ROTARY_MAX_DIM / 4 + 2 <= kMaxThreads, "a workgroup takes at least one head, whose parts may end in vectors");
 constexpr int kAngleBytes = 32768;  // of LDS
 
 // Quotients by a number that is known before the launch, of numbers below 2^31.

@@ -232,7 +232,7 @@ tide_status tide_expert_combine_bwd(int64_t tokens, int32_t choices, int64_t dim
 
 /*
  * Rotary positions of several axes (text: one; image: height, width; video: time, height, width).
- *   tokens, heads, dim  >= 0, >= 0, 1 <= dim <= TIDE_ROTARY_MAX_DIM
+ *   tokens, heads, dim  0 <= tokens < 2^31, 0 <= heads <= TIDE_ROTARY_MAX_HEADS, 1 <= dim <= TIDE_ROTARY_MAX_DIM
  *   x                 device, element (t, h, c) at t * x_token_stride + h * x_head_stride + c; strides >= 0
  *   dtype             of x and out: TIDE_BF16 or TIDE_FP32
  *   positions         device [axes, tokens], contiguous, of positions_dtype (TIDE_INT32, TIDE_INT64 or TIDE_FP32)
@@ -250,7 +250,8 @@ tide_status tide_expert_combine_bwd(int64_t tokens, int32_t choices, int64_t dim
  * Errors: TIDE_ERR_INVALID (null or misaligned pointer, sizes, strides, unknown dtype, pairing or
  * inverse, overlap), TIDE_ERR_HIP.
  */
-#define TIDE_ROTARY_MAX_DIM 2048
+#define TIDE_ROTARY_MAX_HEADS 65535
+#define TIDE_ROTARY_MAX_DIM 1024
 #define TIDE_ROTARY_MAX_AXES 8
 enum { TIDE_ROTARY_HALVES = 0, TIDE_ROTARY_NEIGHBOURS = 1 };
 tide_status tide_rotary(int64_t tokens, int64_t heads, int64_t dim, const void* x, int64_t x_token_stride,

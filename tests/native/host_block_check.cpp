@@ -107,7 +107,7 @@ int main() {
           }
   for (int64_t tokens : sizes)
     for (int64_t heads : sizes)
-      for (int64_t dim : {int64_t(0), int64_t(2), int64_t(128), int64_t(2048), int64_t(2049), lim})
+      for (int64_t dim : {int64_t(0), int64_t(2), int64_t(128), int64_t(1024), int64_t(1025), lim})
         for (int64_t token : sizes)
           for (int64_t head : sizes)
             for (int64_t own : {int64_t(0), dim}) {

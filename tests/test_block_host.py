@@ -125,7 +125,7 @@ def rotary(**kw):
 
 
 def test_rotary_refusals():
-    for kw in (dict(tokens=-1), dict(tokens=1 << 31), dict(heads=-1), dict(heads=1 << 31), dict(dim=0), dict(dim=2049),
+    for kw in (dict(tokens=-1), dict(tokens=1 << 31), dict(heads=-1), dict(heads=1 << 31), dict(heads=65536, tokens=0), dict(dim=0), dict(dim=1025),
                dict(x=None), dict(x=A + 1), dict(xt=-1), dict(xh=-64), dict(xt=1 << 62), dict(dtype=2), dict(pos=None),
                dict(pos=2 * A + 2), dict(pdt=INT64, pos=2 * A + 4), dict(pdt=0), dict(pdt=5), dict(axes=0), dict(axes=9),
                dict(axes=-1), dict(sections=None), dict(sections=i32s(8, 0, 20)), dict(sections=i32s(8, -4, 20)),

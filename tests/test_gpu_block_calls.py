@@ -88,7 +88,7 @@ def test_rotary_refusals(gpu_available):
     ok = dict(x=x, positions=positions, freqs=freqs, sections=(1, 3))
     rotary(**ok)
     for bad in (dict(x=x.double()), dict(x=x[0, 0]), dict(x=x.transpose(1, 2)), dict(x=x.cpu()), dict(x=x[..., :7]),
-                dict(x=x.view(2, 3, 2, 8).transpose(0, 1)), dict(x=torch.zeros(6, 1, 2050, device="cuda")),
+                dict(x=x.view(2, 3, 2, 8).transpose(0, 1)), dict(x=torch.zeros(6, 1, 1026, device="cuda")),
                 dict(positions=positions.double()), dict(positions=positions[:1]), dict(positions=positions[:, :5]),
                 dict(positions=positions.T.contiguous().T), dict(positions=positions[0]), dict(positions=positions.cpu()),
                 dict(freqs=freqs.float()), dict(freqs=freqs[:3]), dict(freqs=freqs.repeat(2)[::2]), dict(freqs=freqs.cpu()),
