@@ -106,43 +106,50 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
   int* before = total + experts;            // [experts]: of lower parts
   int* start = before + experts;            // [experts + 1]: offsets
   int* sums = start + experts + 1;          // [waves]
-  for (int i = threadIdx.x; i < (waves + 2) * experts; i += blockDim.x) count[i] = 0;
   const int64_t end = g.begin(a.pairs, blockIdx.x + 1), first = g.begin(a.pairs, blockIdx.x) + wave * int64_t(g.share);
   const int n = int(first + g.share < end ? g.share : end > first ? end - first : 0);
   const I* ids = static_cast<const I*>(a.ids) + first;
+  I id[kIds];
   int mine[kIds], rank[kIds];
   const auto load = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < kIds; ++j) mine[j] = i0 + j * 64 + lane < n ? expert_of(ids[i0 + j * 64 + lane], experts) : -1;
+    for (int j = 0; j < kIds; ++j) id[j] = i0 + j * 64 + lane < n ? ids[i0 + j * 64 + lane] : I(-1);
   };
-  load(0);
+  const auto find = [&] {
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) mine[j] = expert_of(id[j], experts);
+  };
+  load(0);  // while the counts are read
+  for (int i = threadIdx.x; i < (waves + 2) * experts; i += blockDim.x) count[i] = 0;
   __syncthreads();
   if (parts > 1) {
-    // each thread adds up some of the parts' counts of an expert, or of several
+    // each thread adds up the counts of neighbouring parts for an expert, or for several
     constexpr int kAhead = 16;
     const int groups = blockDim.x > unsigned(experts) ? int(blockDim.x) / experts : 1;
-    const int group = int(threadIdx.x) / experts;
-    if (group < groups)
-      for (int e = int(threadIdx.x) - group * experts; e < experts; e += blockDim.x) {
-        int all = 0, low = 0;
-        for (int b0 = group; b0 < parts; b0 += groups * kAhead) {
-          int c[kAhead];
+    const int group = int(threadIdx.x) / experts, chunk = (parts + groups - 1) / groups, here = int(blockIdx.x);
+    const int b1 = group < groups ? (group * chunk + chunk < parts ? group * chunk + chunk : parts) : 0;
+    for (int e = int(threadIdx.x) - group * experts; e < experts; e += blockDim.x) {
+      int all = 0, low = 0;
+      for (int b0 = group * chunk; b0 < b1; b0 += kAhead) {
+        int c[kAhead], sum = 0;
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int b = b0 + k * groups;
-            c[k] = b < parts ? a.counts[int64_t(b) * experts + e] : 0;
-          }
-          loads_first();
+        for (int k = 0; k < kAhead; ++k) c[k] = b0 + k < b1 ? a.counts[int64_t(b0 + k) * experts + e] : 0;
+        loads_first();
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            all += c[k];
-            if (b0 + k * groups < int(blockIdx.x)) low += c[k];
-          }
+        for (int k = 0; k < kAhead; ++k) sum += c[k];
+        all += sum;
+        if (b0 + kAhead <= here) {
+          low += sum;
+        } else if (b0 < here) {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) low += b0 + k < here ? c[k] : 0;
         }
-        atomicAdd(total + e, all);
-        atomicAdd(before + e, low);
       }
+      if (all > 0) atomicAdd(total + e, all);
+      if (low > 0) atomicAdd(before + e, low);
+    }
   }
+  find();
   // Only this wave uses its row of `count` between barriers, and its LDS accesses stay in order.
   int* own = count + wave * experts;
   // the first place after `at` for the lanes of the same expert, which goes on behind them
@@ -164,7 +171,10 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
     }
   } else {
     for (int i0 = 0; i0 < n; i0 += 64 * kIds) {
-      if (i0 > 0) load(i0);
+      if (i0 > 0) {
+        load(i0);
+        find();
+      }
 #pragma unroll
       for (int j = 0; j < kIds; ++j)
         if (mine[j] >= 0) atomicAdd(own + mine[j], 1);
@@ -210,7 +220,10 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
   }
   __syncthreads();
   for (int i0 = 0; i0 < n; i0 += 64 * kIds) {
-    if (!kHeld) load(i0);
+    if (!kHeld) {
+      load(i0);
+      find();
+    }
 #pragma unroll
     for (int j = 0; j < kIds; ++j) {
       if (i0 + j * 64 >= n) break;
@@ -484,7 +497,7 @@ int sort(const ExpertSortArgs& a, hipStream_t s) {
   const int parts = expert_parts(a.pairs, a.experts);
   SortShape g{ceil_div(ceil_div(a.pairs, parts), 64) * 64, 0, 0};
   int waves = sort_waves(a.experts);
-  while (waves > 1 && g.part <= 32 * waves) waves /= 2;  // at most half of the waves would have pairs
+  while (waves > 1 && g.part <= 64 * waves) waves /= 2;  // 128 pairs a wave, if there are (65536 pairs 8.8 us; 64 a wave 9.4)
   while ((1 << g.bits) < a.experts) ++g.bits;
   g.share = int32_t(ceil_div(ceil_div(g.part, waves), 64) * 64);
   if (parts > 1)

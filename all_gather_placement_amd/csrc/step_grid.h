@@ -22,15 +22,19 @@ __device__ __forceinline__ int tail(int64_t n) {
   return int(n < E ? n : E);
 }
 
+// One step of a scan on the VALU: adds what the lane that kCtrl names has, in the rows of kRows.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp_step(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xf, false);
+}
 // Inclusive sum over the wave.
 __device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
-  return v;
+  v = dpp_step<0x111, 0xf>(v);  // a lane lower, in rows of 16 lanes
+  v = dpp_step<0x112, 0xf>(v);  // 2 lanes
+  v = dpp_step<0x114, 0xf>(v);  // 4
+  v = dpp_step<0x118, 0xf>(v);  // 8
+  v = dpp_step<0x142, 0xa>(v);  // the last lane of row 0 to row 1, of row 2 to row 3
+  return dpp_step<0x143, 0xc>(v);  // the last lane of row 1 to rows 2 and 3
 }
 
 // Lanes of m below this one.
