@@ -473,3 +473,41 @@ def test_dropout_of_many_elements(gpu_available):
     kept = sum(int((part == 2).sum()) for part in got.split(1 << 30))
     # within six deviations of a half (the generator's words are independent fair bits to any such test)
     assert abs(kept - n / 2) < 6 * 0.5 * math.sqrt(n)
+
+
+# ------------------------------------------------------------------------------------------------
+# Far offsets
+# ------------------------------------------------------------------------------------------------
+
+def test_rows_beyond_32_bit_offsets(gpu_available):
+    """A sorted buffer of 2.3e9 elements: its last rows, and the first, as those of a small one."""
+    say("far rows")
+    dim, tokens, take = 16384, 140_000, 40
+    ids = torch.zeros((tokens, 1), dtype=torch.int64, device="cuda")
+    ids[:take] = 1  # the first tokens' rows come last
+    sort = expert_sort(ids, 2)
+    assert int(sort.place[0, 0]) == tokens - take
+    x = torch.zeros((tokens, dim), dtype=BF16, device="cuda")
+    x[:take], x[take:2 * take] = normal((take, dim), BF16, 1), normal((take, dim), BF16, 2)
+    rows = expert_dispatch(x, sort)
+    assert torch.equal(rows[tokens - take:], x[:take]) and torch.equal(rows[:take], x[take:2 * take])
+    w = torch.full((tokens, 1), 2.0, device="cuda")
+    y = expert_combine(rows, w, sort)
+    assert torch.equal(y[:2 * take], 2 * x[:2 * take]) and not bool(y[-take:].any())
+    del y
+    drows, dw = expert_combine_bwd(x, rows, w, sort, drows=rows)
+    assert drows is rows and torch.equal(rows[tokens - take:], 2 * x[:take]) and torch.equal(rows[:take], 2 * x[take:2 * take])
+    size = x[:2 * take].double().square().sum(1)
+    within(dw[:2 * take, 0], size, dim * U * size, "dweights")
+
+
+def test_heads_beyond_32_bit_offsets(gpu_available):
+    say("far heads")
+    tokens, heads, dim, sections = 70_000, 128, 256, (60, 68)
+    x = torch.zeros((tokens, heads, dim), dtype=BF16, device="cuda")
+    x[-8:], x[:8] = normal((8, heads, dim), BF16, 1), normal((8, heads, dim), BF16, 2)
+    positions, freqs = positions_of(tokens, 2, torch.int64, 3), rotary_freqs(sections)
+    ends = [(part, rotary(x[part], positions[:, part].contiguous(), freqs, sections).clone()) for part in (slice(0, 8), slice(tokens - 8, tokens))]
+    rotary(x, positions, freqs, sections, out=x)
+    for part, want in ends:
+        assert torch.equal(x[part], want)
