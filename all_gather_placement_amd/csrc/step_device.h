@@ -193,6 +193,26 @@ __device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[E]) {
       if (i < n) p[i] = narrow<T>(f[i]);
   }
 }
+// The first n (of E) elements of r to p, bit for bit; kWhole as for load_vec.
+template <typename T, int E, bool kOnce, bool kWhole>
+__device__ __forceinline__ void store_raw(T* p, int n, const Raw<T, E>& r) {
+  if (n >= E) {
+    static_assert(Raw<T, E>::kWords % 4 == 0, "stores are of 16 bytes");
+#pragma unroll
+    for (int q = 0; q < Raw<T, E>::kWords / 4; ++q)
+      store16<kOnce>(reinterpret_cast<char*>(p) + 16 * q,
+                     u32x4{r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]});
+  } else if constexpr (!kWhole) {
+#pragma unroll
+    for (int i = 0; i < E - 1; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2)
+          p[i] = T(i & 1 ? r.w[i / 2] >> 16 : r.w[i / 2]);
+        else
+          p[i] = __uint_as_float(r.w[i]);
+      }
+  }
+}
 // f(whole) as a constant: rows of `cols` elements are of whole vectors of E, or not.
 template <int E, typename F>
 int with_whole(int64_t cols, F&& f) {

@@ -22,6 +22,7 @@ namespace tide_step {
 namespace {
 
 constexpr int kThreads = 256;
+
 // ---------------------------------------------------------------------------------------------
 // Sort
 // ---------------------------------------------------------------------------------------------
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
   find();
   // Only this wave uses its row of `count` between barriers, and its LDS accesses stay in order.
   int* own = count + wave * experts;
-  // the first place after `at` for the lanes of the same expert, which goes on behind them
+  // the next places of the lanes' experts, in order of the lanes; own[e] goes on behind them
   const auto take = [&](int e) {
     const uint64_t same = same_expert(e, g.bits);
     int at = -1;
@@ -277,6 +278,10 @@ struct Columns {
   __device__ __forceinline__ void store(T* row, const float (&f)[E]) const {
     store_vec<T, E, kOnce, !kTiny>(row + at, n, f);
   }
+  template <bool kOnce>
+  __device__ __forceinline__ void store(T* row, const Raw<T, E>& r) const {
+    store_raw<T, E, kOnce, !kTiny>(row + at, n, r);
+  }
 };
 
 // A lane's place: 1 << lshift neighbouring lanes of the workgroup share a row, whole waves of it from 64 on.
@@ -322,7 +327,7 @@ __device__ __forceinline__ void zero_rows(const ExpertRowsArgs& a, int count, un
   constexpr int E = kVec<T>, kWaves = kThreads / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t pairs = a.tokens * a.choices;
-  const float zero[E] = {};
+  const Raw<T, E> zero = {};
   const int64_t apart = int64_t(wgs) * kWaves;
   for (int64_t r0 = int64_t(wg) * kWaves + wave; r0 < a.rows; r0 += apart * count) {
     bool none = false;
@@ -352,12 +357,9 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(ExpertRowsArg
     for (int64_t c = int64_t(l.lane) * E; c < a.dim; c += int64_t(E) << lshift) {
       const Columns<T, kTiny> col(c, a.dim);
       const Raw<T, E> v = col.template load<true>(from);
-      float f[E];
-#pragma unroll
-      for (int k = 0; k < E; ++k) f[k] = v.get(k);
       for (int j = 0; j < a.choices; ++j) {
         const int row = place[j];
-        if (row >= 0 && row < a.rows) col.template store<kOnce>(static_cast<T*>(a.out) + row * a.out_stride, f);
+        if (row >= 0 && row < a.rows) col.template store<kOnce>(static_cast<T*>(a.out) + row * a.out_stride, v);
       }
     }
   }

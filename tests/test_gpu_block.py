@@ -230,6 +230,19 @@ def test_gradients_of_experts_are_differences(gpu_available):
         assert torch.equal(expert_combine(expert_dispatch(x[:4], sort), None, sort), x[:4] * choices)
 
 
+@pytest.mark.parametrize("dim", [3, 8, 77])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_dispatch_moves_bits(gpu_available, dtype, dim):
+    """Every bit pattern: denormal numbers and what a NaN carries."""
+    bits = torch.int16 if dtype == BF16 else torch.int32
+    low, high = torch.iinfo(bits).min, torch.iinfo(bits).max
+    x = torch.randint(low, high, (900, dim), device="cuda", generator=gen(1)).to(bits)
+    sort = expert_sort(make_ids(900, 2, 7, "some", 2), 7)
+    rows = expert_dispatch(x.view(dtype), sort).view(bits)
+    real = sort.source >= 0
+    assert torch.equal(rows[real], x[sort.source[real].long() // 2]) and not bool(rows[~real].any())
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_experts_special_values(gpu_available, dtype):
     sort = expert_sort(torch.tensor([[0, -1], [1, 0], [-1, -1]], device="cuda"), 2, align=4)
