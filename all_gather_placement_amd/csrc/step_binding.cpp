@@ -672,16 +672,15 @@ PyObject* rotary(Args a, Py_ssize_t n) {
   int64_t pairs = 0;
   int32_t axes = 0;
   {  // before addresses are taken: whole() may run Python code
-    const Held seq(PySequence_Fast(a[3], "sections must be a sequence of whole numbers"));
+    const Held seq(PySequence_Tuple(a[3]));
     if (seq.o == nullptr) throw Refused();
-    const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq.o);
+    const Py_ssize_t count = PyTuple_GET_SIZE(seq.o);
     NEED(count >= 1 && count <= TIDE_ROTARY_MAX_AXES, "there must be 1 to ", TIDE_ROTARY_MAX_AXES, " sections, got ", count);
     for (; axes < count; ++axes) {
-      const int64_t v = whole(PySequence_Fast_GET_ITEM(seq.o, axes));
+      const int64_t v = whole(PyTuple_GET_ITEM(seq.o, axes));
       NEED(v >= 1 && v <= TIDE_ROTARY_MAX_DIM, "each section must have 1 to ", TIDE_ROTARY_MAX_DIM, " pairs, got ", v);
       sections[axes] = int32_t(v);
       pairs += v;
-      NEED(axes + 1 == count || PySequence_Fast_GET_SIZE(seq.o) == count, "sections must not change");
     }
   }
   const bool halves = PyUnicode_Check(a[4]) && PyUnicode_CompareWithASCIIString(a[4], "halves") == 0;
