@@ -17,8 +17,8 @@ namespace tide_step {
 namespace {
 
 // Items of a thread: all of its loads are in flight before the angles are made, and none waits for a store.
-template <bool kHalves, bool kWhole>
-constexpr int kItems = (kHalves ? 2 : 4) / (kWhole ? 1 : 2);
+template <bool kHalves>
+constexpr int kItems = kHalves ? 2 : 4;
 // A thread has fewer items where it would make more than four angles for them, which all wait for each other (100000
 // tokens of one head of 64 bf16 11.6 us instead of 13.9), and where there would be few workgroups (512 tokens of 32
 // heads of 128 3.6 us instead of 4.1).
@@ -77,18 +77,40 @@ __device__ __forceinline__ void turn(double angle, float* cos, float* sin) {
 }
 
 // A vector, or the two vectors that are turned against each other.
-template <typename T, bool kHalves>
+template <typename T>
 struct Item {
-  static constexpr int E = kVec<T>;
   uint32_t t, u;
   T* to;
-  Raw<T, E> first, second;
+  Raw<T, kVec<T>> first, second;
 };
 
-// kWhole: the turned elements and the others are of whole vectors.  kOnce: they are read past the caches.
-template <typename T, typename P, bool kHalves, bool kWhole, bool kOnce>
+// Where a part of a head -- the turned elements, of halves each half; the others -- is no whole number of vectors, its
+// last vector is the one that ends with it, and shares elements with the one before: both lanes turn them and write the
+// same values.  In place, a lane must not read what another has turned: a workgroup has all of a head, and its loads
+// are complete before its barrier, its stores behind it.
+template <int E, bool kWhole>
+__device__ __forceinline__ int vector_at(int c, int length) {
+  return kWhole || c + E <= length ? c : length - E;
+}
+// The same for a part of less than a vector, its elements.
+template <typename T, bool kTiny, bool kOnce>
+__device__ __forceinline__ Raw<T, kVec<T>> load_part(const T* p, int length) {
+  if (!kTiny || length >= kVec<T>) return load_whole<T, kVec<T>, kOnce>(p);
+  return load_vec<T, kVec<T>, kOnce, false>(p, length, false);
+}
+template <typename T, bool kTiny, bool kOnce>
+__device__ __forceinline__ void store_part(T* p, int length, const float (&f)[kVec<T>]) {
+  store_vec<T, kVec<T>, kOnce, !kTiny>(p, kTiny ? length : kVec<T>, f);
+}
+
+// How the parts of a head end: with whole vectors, inside one, or before the first.
+enum Ends { kWholeVectors, kInsideVectors, kTinyParts };
+
+// kOnce: vectors are read past the caches.
+template <typename T, typename P, bool kHalves, Ends kEnds, bool kOnce>
 __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, RotaryShape g) {
-  constexpr int E = kVec<T>, N = kItems<kHalves, kWhole>;
+  constexpr int E = kVec<T>, N = kItems<kHalves>;
+  constexpr bool kWhole = kEnds == kWholeVectors, kTiny = kEnds == kTinyParts;
   extern __shared__ f32x4 lds[];
   float* cosines = reinterpret_cast<float*>(lds);  // [tokens][padded]
   float* sines = cosines + g.tokens * g.padded;
@@ -97,7 +119,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
   const int turned = 2 * a.pairs, plain = a.dim - turned;
   const int64_t t0 = g.first_token + int64_t(blockIdx.x) * g.tokens;
   const uint32_t tokens = uint32_t(a.tokens - t0 < g.tokens ? a.tokens - t0 : g.tokens);
-  Item<T, kHalves> item[N];
+  Item<T> item[N];
   bool there[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
@@ -110,15 +132,15 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
     item[j].to = static_cast<T*>(a.out) + (t0 + t) * a.out_token + (h0 + h) * a.out_head;
     if (!there[j]) continue;
     if (int(u) >= g.units) {
-      const int c = (int(u) - g.units) * E;
-      item[j].first = load_vec<T, E, kOnce, kWhole>(from + turned + c, tail<E>(plain - c), plain >= E);
+      const int c = vector_at<E, kWhole || kTiny>((int(u) - g.units) * E, plain);
+      item[j].first = load_part<T, kTiny, kOnce>(from + turned + c, kTiny ? plain - c : plain);
     } else if constexpr (kHalves) {
-      const int c = int(u) * E, n = tail<E>(a.pairs - c);
-      item[j].first = load_vec<T, E, kOnce, kWhole>(from + c, n, a.pairs >= E);
-      item[j].second = load_vec<T, E, kOnce, kWhole>(from + a.pairs + c, n, a.pairs >= E);
+      const int c = vector_at<E, kWhole || kTiny>(int(u) * E, a.pairs);
+      item[j].first = load_part<T, kTiny, kOnce>(from + c, kTiny ? a.pairs - c : a.pairs);
+      item[j].second = load_part<T, kTiny, kOnce>(from + a.pairs + c, kTiny ? a.pairs - c : a.pairs);
     } else {
-      const int c = int(u) * E;
-      item[j].first = load_vec<T, E, kOnce, kWhole>(from + c, tail<E>(turned - c), turned >= E);
+      const int c = vector_at<E, kWhole || kTiny>(int(u) * E, turned);
+      item[j].first = load_part<T, kTiny, kOnce>(from + c, kTiny ? turned - c : turned);
     }
   }
   loads_first();
@@ -132,22 +154,30 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
     cosines[t * g.padded + p] = c;
     sines[t * g.padded + p] = s * a.sign;
   }
+  if constexpr (kEnds == kInsideVectors) {  // the loads are complete
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (there[j]) {
+        item[j].first.forget();
+        if constexpr (kHalves) item[j].second.forget();
+      }
+  }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (!there[j]) continue;
     const int u = int(item[j].u);
     if (u >= g.units) {
-      const int c = (u - g.units) * E;
+      const int c = vector_at<E, kWhole || kTiny>((u - g.units) * E, plain);
       float f[E];
 #pragma unroll
       for (int k = 0; k < E; ++k) f[k] = item[j].first.get(k);
-      store_vec<T, E, kWhole, kWhole>(item[j].to + turned + c, tail<E>(plain - c), f);
+      store_part<T, kTiny, kWhole>(item[j].to + turned + c, plain - c, f);
       continue;
     }
     constexpr int A = kAnglesOf<T, kHalves>;
-    typedef float Angles __attribute__((ext_vector_type(A)));
-    const int p = u * A;
+    typedef float Angles __attribute__((ext_vector_type(A), aligned(kWhole ? 4 * A : 4)));
+    const int p = vector_at<A, kWhole || kTiny>(u * A, a.pairs);
     const Angles c = *reinterpret_cast<const Angles*>(cosines + item[j].t * g.padded + p);
     const Angles s = *reinterpret_cast<const Angles*>(sines + item[j].t * g.padded + p);
     if constexpr (kHalves) {
@@ -158,9 +188,8 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
         f[k] = x * c[k] - y * s[k];
         f2[k] = y * c[k] + x * s[k];
       }
-      const int n = tail<E>(a.pairs - p);
-      store_vec<T, E, kWhole, kWhole>(item[j].to + p, n, f);
-      store_vec<T, E, kWhole, kWhole>(item[j].to + a.pairs + p, n, f2);
+      store_part<T, kTiny, kWhole>(item[j].to + p, a.pairs - p, f);
+      store_part<T, kTiny, kWhole>(item[j].to + a.pairs + p, a.pairs - p, f2);
     } else {
       float f[E];
 #pragma unroll
@@ -169,14 +198,14 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
         f[2 * k] = x * c[k] - y * s[k];
         f[2 * k + 1] = y * c[k] + x * s[k];
       }
-      store_vec<T, E, kWhole, kWhole>(item[j].to + 2 * p, tail<E>(turned - 2 * p), f);
+      store_part<T, kTiny, kWhole>(item[j].to + 2 * p, turned - 2 * p, f);
     }
   }
 }
 
-template <typename T, typename P, bool kHalves, bool kWhole, bool kOnce>
+template <typename T, typename P, bool kHalves, Ends kEnds, bool kOnce>
 int rotary(const RotaryArgs& a, hipStream_t s) {
-  constexpr int E = kVec<T>, N = kItems<kHalves, kWhole>;
+  constexpr int E = kVec<T>, N = kItems<kHalves>;
   const int units = int(kHalves ? ceil_div(a.pairs, E) : ceil_div(2 * a.pairs, E));
   const int copied = a.x == a.out ? 0 : int(ceil_div(a.dim - 2 * a.pairs, E));
   const int padded = int(ceil_div(a.pairs, E) * E);
@@ -200,7 +229,7 @@ int rotary(const RotaryArgs& a, hipStream_t s) {
   // workgroups have one turn: more tokens than a launch holds take another
   int e = 0;
   for (; g.first_token < a.tokens && e == 0; g.first_token += kMaxGrid * tokens)
-    e = launch(rotary_kernel<T, P, kHalves, kWhole, kOnce>,
+    e = launch(rotary_kernel<T, P, kHalves, kEnds, kOnce>,
                dim3(grid_of(a.tokens - g.first_token, tokens), unsigned(ceil_div(a.heads, heads))), int(threads),
                size_t(tokens) * padded * 8, s, a, g);
   return e;
@@ -213,10 +242,11 @@ constexpr int64_t kPastCaches = int64_t(256) << 20;
 template <typename T, typename P, bool kHalves>
 int rotary(const RotaryArgs& a, hipStream_t s) {
   constexpr int E = kVec<T>;
-  const bool whole = (kHalves ? a.pairs : 2 * a.pairs) % E == 0 && (a.x == a.out || (a.dim - 2 * a.pairs) % E == 0);
-  if (!whole) return rotary<T, P, kHalves, false, false>(a, s);
+  const int part = kHalves ? a.pairs : 2 * a.pairs, plain = a.x == a.out ? 0 : a.dim - 2 * a.pairs;
+  if (part < E || (plain > 0 && plain < E)) return rotary<T, P, kHalves, kTinyParts, false>(a, s);
+  if (part % E != 0 || plain % E != 0) return rotary<T, P, kHalves, kInsideVectors, false>(a, s);
   const bool once = 2 * a.tokens * a.heads * a.dim * int64_t(sizeof(T)) > kPastCaches;
-  return once ? rotary<T, P, kHalves, true, true>(a, s) : rotary<T, P, kHalves, true, false>(a, s);
+  return once ? rotary<T, P, kHalves, kWholeVectors, true>(a, s) : rotary<T, P, kHalves, kWholeVectors, false>(a, s);
 }
 template <typename T, typename P>
 int rotary(const RotaryArgs& a, int pairing, hipStream_t s) {

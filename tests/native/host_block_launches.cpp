@@ -192,10 +192,9 @@ static void turns() {
               for (bool in_place : {false, true}) {
                 if (pairs < 1 || 2 * pairs > dim || heads > (int64_t(1) << 44) / dim / tokens) continue;
                 const int e = dtype == TIDE_BF16 ? 8 : 4, turned = pairing == TIDE_ROTARY_HALVES ? pairs : 2 * pairs;
-                const bool whole = turned % e == 0 && (in_place || (dim - 2 * pairs) % e == 0);
                 call_tokens = tokens;
                 call_items = (turned + e - 1) / e + (in_place ? 0 : (dim - 2 * pairs + e - 1) / e);
-                items_of_thread = (pairing == TIDE_ROTARY_HALVES ? 2 : 4) / (whole ? 1 : 2);
+                items_of_thread = pairing == TIDE_ROTARY_HALVES ? 2 : 4;
                 next_token = 0;
                 on_launch = count_tokens;
                 const tide_status s = rotary(tokens, heads, dim, pairs, pairing, dtype, in_place);

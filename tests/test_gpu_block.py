@@ -291,7 +291,8 @@ def test_numbers_that_no_sort_gives_touch_nothing_outside(gpu_available):
 ROTARY = [(1, 1, 2, (1,)), (1, 32, 128, (64,)), (5, 3, 6, (1, 2)), (70, 4, 64, (8, 12, 12)), (33, 7, 80, (17, 19)),
           (300, 2, 96, (16, 16, 16)), (9, 40, 128, (22, 21, 21)), (129, 1, 256, (128,)), (11, 5, 100, (3, 4, 5, 6)),
           (2, 1, 1024, (125, 387)), (3, 2, 1021, (1,)), (3, 130, 40, (20,)), (1000, 1, 10, (1, 1, 1, 1, 1)), (4, 9, 31, (7, 8)),
-          (2, 3, 18, (1, 1, 1, 1, 1, 1, 1, 1)), (50, 3, 576, (32,))]
+          (2, 3, 18, (1, 1, 1, 1, 1, 1, 1, 1)), (50, 3, 576, (32,)), (257, 20, 90, (39,)),
+          (100, 33, 59, (21,)), (65, 40, 126, (20, 21, 22))]
 
 
 def positions_of(tokens, axes, kind, seed):
