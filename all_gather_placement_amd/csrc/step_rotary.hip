@@ -235,8 +235,8 @@ int rotary(const RotaryArgs& a, hipStream_t s) {
   return e;
 }
 // More than the last-level cache holds, read and written, is read past it: 32760 x 40 x 128 bf16 108 us instead of
-// 112, a seventh of that 17.5 instead of 16.2.  Vectors that end inside others' cache lines need the caches (50000 x 8
-// x 100 with 64 turned 33 us, past them 56).
+// 112, a seventh of that 17.5 instead of 16.2.  Loads of vectors that end inside others' cache lines need the caches
+// (50000 x 8 x 100 with 64 turned 34 us, past them 43).
 constexpr int64_t kPastCaches = int64_t(256) << 20;
 
 template <typename T, typename P, bool kHalves>
