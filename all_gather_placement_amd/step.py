@@ -287,7 +287,8 @@ def rotary(x, positions, freqs, sections, pairing="halves", out=None, stream=Non
 
 
 def rotary_bwd(dy, positions, freqs, sections, pairing="halves", out=None, stream=None):
-    """Gradient of :func:`rotary` with respect to x: dy turned back.  `out` may be dy itself."""
+    """Gradient of :func:`rotary` with respect to x: dy turned back.  `out` may be dy itself.  Heads that were one
+    vector read several times (an expanded x) have a gradient each; their sum is that vector's."""
     if stream is None:
         return (_step or load_step_binding()).rotary(dy, positions, freqs, sections, pairing, True, out)
     return _call("rotary", stream, dy, positions, freqs, sections, pairing, True, out)
