@@ -30,7 +30,9 @@ constexpr int kThreads = 256;
 // Each wave of a workgroup counts its own pairs of each expert: as many waves as 32 KiB of LDS hold the
 // counts of.
 constexpr int kCountBytes = 32768;
-constexpr int kIds = 8;  // of a lane at a time
+// Of a lane at a time: the code for each is long, and more of it takes longer than it saves (524288 pairs 13.0 us, with 8
+// ids 13.4; 4096 pairs 8.4 and 9.2; 524288 of 2048 experts, many rounds, 72 and 65).
+constexpr int kIds = 2;
 constexpr int kExpertBits = 11;
 static_assert(TIDE_MAX_EXPERTS <= 1 << kExpertBits, "bits of an expert's number");
 inline int sort_waves(int experts) {
@@ -499,7 +501,7 @@ int sort(const ExpertSortArgs& a, hipStream_t s) {
   const int parts = expert_parts(a.pairs, a.experts);
   SortShape g{ceil_div(ceil_div(a.pairs, parts), 64) * 64, 0, 0};
   int waves = sort_waves(a.experts);
-  while (waves > 1 && g.part <= 64 * waves) waves /= 2;  // 128 pairs a wave, if there are (65536 pairs 8.8 us; 64 a wave 9.4)
+  while (waves > 1 && g.part <= 64 * waves) waves /= 2;  // 128 pairs a wave, if there are (65536 pairs 8.8 us with 8 ids a lane; 64 a wave 9.4)
   while ((1 << g.bits) < a.experts) ++g.bits;
   g.share = int32_t(ceil_div(ceil_div(g.part, waves), 64) * 64);
   if (parts > 1)
