@@ -256,8 +256,9 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
 // ---------------------------------------------------------------------------------------------
 
 // A row's columns in vectors of E, one a lane.  Where a row ends inside a vector, the last one is the vector that
-// ends with the row: it shares elements with the one before, which both read, and write alike.  Loads and stores of
-// single elements, and their waits, would take longer than the rest of a row.  kTiny: rows of less than a vector.
+// ends with the row: it shares elements with the one before, which both read, and write alike -- but not over what they
+// read, where the one before may be late: another wave's, or an earlier turn's.  Loads and stores of single elements, and
+// their waits, would take longer than the rest of a row.  kTiny: rows of less than a vector.
 template <typename T, bool kTiny>
 struct Columns {
   static constexpr int E = kVec<T>;
@@ -279,6 +280,12 @@ struct Columns {
   template <bool kOnce>
   __device__ __forceinline__ void store(T* row, const float (&f)[E]) const {
     store_vec<T, E, kOnce, !kTiny>(row + at, n, f);
+  }
+  // The same without the elements of the vector before.
+  __device__ __forceinline__ void store_own(T* row, const float (&f)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k >= shared && k < n) row[at + k] = narrow<T>(f[k]);
   }
   template <bool kOnce>
   __device__ __forceinline__ void store(T* row, const Raw<T, E>& r) const {
@@ -424,7 +431,9 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(ExpertRowsArgs
 // of whole waves are read and written past the caches, beside the zeros, which go through them: 8192 x 2048 bf16 by
 // eight experts 110 us, through the caches 129, a quarter of that 38 and 47; rows of 100 columns 19 us, past the
 // caches 21.
-template <typename T, int N, bool kTiny, int kLanes>
+// kOwn: an element is written by the lane that has it in its dot product, and read by no other for its own.  Rows that end
+// inside a vector need that in place; a form of its own, since the other takes 2% longer with a branch for it.
+template <typename T, int N, bool kTiny, int kLanes, bool kOwn>
 __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRowsArgs a, bool bf16_weights,
                                                                       Mixed mixed, int wshift, int zero_count) {
   constexpr int E = kVec<T>;
@@ -466,7 +475,11 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(ExpertRows
               if (kTiny || k >= col.shared) dot[j] = fmaf(d.get(k), r[j].get(k), dot[j]);
               f[k] = ch.w[j] * d.get(k);
             }
-            col.template store<(kLanes == 64)>(static_cast<T*>(a.out) + ch.row[j] * a.out_stride, f);
+            T* to = static_cast<T*>(a.out) + ch.row[j] * a.out_stride;
+            if (kOwn && col.shared > 0)
+              col.store_own(to, f);
+            else
+              col.template store<(kLanes == 64)>(to, f);
           }
           if constexpr (kLanes < 64) break;  // lanes for all of a row
         }
@@ -568,19 +581,22 @@ int combine(const ExpertRowsArgs& a, bool bf16_weights, hipStream_t s) {
 template <typename T>
 int combine_bwd(const ExpertRowsArgs& a, bool bf16_weights, hipStream_t s) {
   const int64_t vecs = ceil_div(a.dim, kVec<T>);
-  const auto call = [&](auto tiny, auto lanes) {
+  const auto call = [&](auto tiny, auto lanes, auto own) {
     return with_choices(a.choices, [&](auto n) {
       const int wshift = vecs <= 64 ? 0 : vecs <= 128 ? 1 : 2;
       const Mixed mixed(a.tokens > 0 ? grid_of(a.tokens, (kThreads / decltype(lanes)::value) >> wshift) : 0,
                         zeroing_of(a, vecs));
-      return launch(expert_combine_bwd_kernel<T, decltype(n)::value, decltype(tiny)::value, decltype(lanes)::value>,
+      return launch(expert_combine_bwd_kernel<T, decltype(n)::value, decltype(tiny)::value, decltype(lanes)::value,
+                                              decltype(own)::value>,
                     mixed.tokens + mixed.zeros, kThreads, 0, s, a, bf16_weights, mixed, wshift, zero_rows_of(vecs));
     });
   };
-  if (a.dim < kVec<T>) return call(std::true_type(), std::integral_constant<int, 1>());
-  if (vecs <= 4) return call(std::false_type(), std::integral_constant<int, 4>());
-  if (vecs <= 16) return call(std::false_type(), std::integral_constant<int, 16>());
-  return call(std::false_type(), std::integral_constant<int, 64>());
+  if (a.dim < kVec<T>) return call(std::true_type(), std::integral_constant<int, 1>(), std::false_type());
+  return with_bool(a.out == a.x && a.dim % kVec<T> != 0, [&](auto own) {
+    if (vecs <= 4) return call(std::false_type(), std::integral_constant<int, 4>(), own);
+    if (vecs <= 16) return call(std::false_type(), std::integral_constant<int, 16>(), own);
+    return call(std::false_type(), std::integral_constant<int, 64>(), own);
+  });
 }
 
 }  // namespace
