@@ -245,7 +245,9 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
   // rows of no pair: 16 lanes for each expert's, all for those behind the last expert
   if (a.align > 1)
     for (int e = int((blockIdx.x * blockDim.x + threadIdx.x) >> 4); e < experts; e += int((gridDim.x * blockDim.x) >> 4))
-      for (int r = start[e] + total[e] + int(threadIdx.x & 15); r < start[e + 1]; r += 16) a.source[r] = -1;
+      // without a sign: the last of 2^31 - 1 rows may be an expert's, or end where another's begin
+      for (unsigned r = unsigned(start[e] + total[e]) + (threadIdx.x & 15); r < unsigned(start[e + 1]); r += 16)
+        a.source[r] = -1;
   for (int64_t r = start[experts] + int64_t(blockIdx.x) * blockDim.x + threadIdx.x; r < a.rows;
        r += int64_t(parts) * blockDim.x)
     a.source[r] = -1;

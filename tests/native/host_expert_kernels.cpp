@@ -2,6 +2,12 @@
 // Exit status 0 = all checks passed.
 //
 //   host_expert_kernels in_place   gradients written over the rows that they are made of
+//   host_expert_kernels sort       places, rows and offsets of small calls
+//   host_expert_kernels far        a sort whose rows end at the largest number
+#include <sys/mman.h>
+#include <unistd.h>
+
+#include <algorithm>
 #include <cstdio>
 #include <random>
 #include <string>
@@ -88,6 +94,44 @@ void in_place(int dtype, int64_t dim, int choices) {
         (long long)dim, choices, lanes::backwards ? "last lanes first" : "first lanes first", wrong_dots, (long long)pairs, wrong_rows);
 }
 
+template <typename I>
+void sorted(int dtype, int64_t tokens, int choices, int experts, int align, int more) {
+  const int64_t pairs = tokens * choices, rows = pairs + std::min<int64_t>(experts, pairs) * (align - 1) + more;
+  std::mt19937 rng(unsigned(pairs + experts));
+  std::vector<I> ids(static_cast<size_t>(pairs));
+  for (I& id : ids) id = I(int(rng() % unsigned(experts + 2)) - 1);
+  std::vector<int32_t> place(size_t(pairs), 77), source(size_t(rows + 1), 77), offsets(size_t(experts) + 1, 77);
+  std::vector<int32_t> counts(size_t(expert_parts(pairs, experts)) * size_t(experts));
+  launch_expert_sort({pairs, ids.data(), experts, align, place.data(), source.data(), rows, offsets.data(), counts.data()}, dtype, nullptr);
+  std::vector<int32_t> p(size_t(pairs), -1), s(size_t(rows + 1), -1), o(size_t(experts) + 1, 0);
+  s.back() = 77;
+  for (int e = 0; e < experts; ++e) {
+    int32_t at = o[size_t(e)];
+    for (int64_t i = 0; i < pairs; ++i)
+      if (ids[size_t(i)] == e) p[size_t(i)] = at, s[size_t(at++)] = int32_t(i);
+    o[size_t(e) + 1] = (at + align - 1) / align * align;
+  }
+  CHECK(place == p && source == s && offsets == o, "%lld tokens, %d choices of %d, multiples of %d", (long long)tokens, choices, experts, align);
+}
+
+// One pair of two experts, whose rows are rounded up to the largest number: the first expert's rows end there, and
+// the second's begin.  All of the rows' memory is one piece, mapped over and over; none of what lies before and behind
+// it may be touched.
+void far() {
+  const int64_t rows = (int64_t(1) << 31) - 1, bytes = int64_t(1) << 33, piece = int64_t(1) << 23;
+  char* space = static_cast<char*>(mmap(nullptr, size_t(4 * bytes), PROT_NONE, MAP_PRIVATE | MAP_ANONYMOUS | MAP_NORESERVE, -1, 0));
+  const int file = memfd_create("rows", 0);
+  CHECK(space != MAP_FAILED && file >= 0 && ftruncate(file, piece) == 0, "no memory");
+  if (failures > 0) return;
+  char* from = space + 2 * bytes;
+  for (int64_t at = 0; at < bytes; at += piece)
+    CHECK(mmap(from + at, size_t(piece), PROT_READ | PROT_WRITE, MAP_SHARED | MAP_FIXED, file, 0) != MAP_FAILED, "no memory");
+  const int64_t id = 0;
+  int32_t place = 77, offsets[3] = {77, 77, 77};
+  launch_expert_sort({1, &id, 2, int32_t(rows), &place, reinterpret_cast<int32_t*>(from), rows, offsets, nullptr}, TIDE_INT64, nullptr);
+  CHECK(place == 0 && offsets[0] == 0 && offsets[1] == rows && offsets[2] == rows, "%d %d %d", place, offsets[1], offsets[2]);
+}
+
 int main(int argc, char** argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   if (what == "in_place") {
@@ -102,6 +146,16 @@ int main(int argc, char** argv) {
           in_place<bf16_t>(TIDE_BF16, dim, choices);
       }
     }
+  } else if (what == "sort") {
+    for (int more : {0, 5})
+      for (int align : {1, 7, 16, 128})
+        for (int experts : {1, 2, 9, 63, 200}) {
+          for (int64_t tokens : {0, 1, 5, 70, 333}) sorted<int64_t>(TIDE_INT64, tokens, 3, experts, align, more);
+          sorted<int32_t>(TIDE_INT32, 2100, 2, experts, align, more);
+        }
+    sorted<int32_t>(TIDE_INT32, 5000, 1, 2048, 3, 1);
+  } else if (what == "far") {
+    far();
   } else {
     ++failures;
   }

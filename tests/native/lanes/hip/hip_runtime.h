@@ -54,11 +54,11 @@ inline std::function<void()> kernel;
 inline void rest() { swapcontext(&group[current].context, &scheduler); }
 template <typename Reached>
 void wait_for(unsigned from, unsigned to, Reached&& reached) {
-  for (;;) {
-    bool all = true;
+  ++moves;
+  for (bool all = false; !all;) {
+    rest();  // also the last one, so that lanes go on in their order
+    all = true;
     for (unsigned i = from; i < to && i < group.size(); ++i) all &= group[i].done || reached(group[i]);
-    if (all) break;
-    rest();
   }
   ++moves;
 }

@@ -22,7 +22,7 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("what", ["in_place"])
+@pytest.mark.parametrize("what", ["in_place", "sort", "far"])
 def test_kernels(program, what):
     res = subprocess.run([program, what], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0 and "0 failures" in res.stdout, res.stdout + res.stderr[-4000:]
