@@ -50,11 +50,13 @@ struct RotaryShape {
   Divisor pairs;
 };
 
-// cos and sin of an angle, as their values rounded to fp32.  In 64 bits, far positions keep their place within a
-// turn; what is left of the angle beside whole quarters is at most pi / 4, where the series of sine and cosine up
-// to the 11th and 12th power are within 2^-36.
+// cos and sin of an angle of up to 2^64, as their values rounded to fp32.  Whole turns are taken off the product with
+// 1 / (2 pi) before it is rounded, and that factor has two parts: far positions keep their place within a turn to 2^-43.
+// What is left of the angle beside whole quarters is at most pi / 4, where the series of sine and cosine up to the 11th
+// and 12th power are within 2^-36.
 __device__ __forceinline__ void turn(double angle, float* cos, float* sin) {
-  double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
+  constexpr double kTurn = 0.15915494309189533577, kTurnRest = -9.839338337591243e-18;  // 1 / (2 pi)
+  double turns = fma(angle, kTurnRest, fma(angle, kTurn, -rint(angle * kTurn)));
   turns -= rint(turns);
   const double quarters = rint(4.0 * turns);
   const double x = fma(-0.25, quarters, turns) * 6.28318530717958647692, y = x * x;

@@ -274,7 +274,7 @@ def rotary_freqs(sections, base=10000.0, shared=False, device=None):
 
 
 def rotary(x, positions, freqs, sections, pairing="halves", out=None, stream=None):
-    """Pairs of a head's elements turned by positions[axis] * freqs[pair], the angle taken in 64 bits.
+    """Pairs of a head's elements turned by positions[axis] * freqs[pair], the angle (up to 2^64) taken in 64 bits.
 
     x is [..., heads, dim], bf16 or fp32, contiguous, or [tokens, heads, dim] whose vectors are; `out` may be
     x itself.  positions is [axes, ...] for the tokens, contiguous int32, int64 or fp32 (text: one axis;

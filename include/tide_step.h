@@ -244,9 +244,10 @@ tide_status tide_expert_combine_bwd(int64_t tokens, int32_t choices, int64_t dim
  *   inverse           0, or 1 to turn back: the gradient with respect to x
  *   out               device, as x with strides of its own, its elements apart from each other; may be x
  *                     itself with the same strides (in place)
- * Result: with a = positions[axis of i][t] * freqs[i] in 64 bits (minus that for inverse) and cos a, sin a
- * rounded to fp32, pair (u, v) becomes (u cos a - v sin a, v cos a + u sin a) in fp32, rounded once.
- * Elements from 2 P on are copied.  A position that is infinite or NaN gives NaN.
+ * Result: with a = positions[axis of i][t] * freqs[i], both as fp64 and their product (minus that for inverse),
+ * and cos a, sin a rounded to fp32, off by less than 2^-35 before that, pair (u, v) becomes
+ * (u cos a - v sin a, v cos a + u sin a) in fp32, rounded once.  That holds for |a| up to 2^64; beyond, a sine and
+ * cosine of some angle are taken.  Elements from 2 P on are copied.  A position that is infinite or NaN gives NaN.
  * Errors: TIDE_ERR_INVALID (null or misaligned pointer, sizes, strides, unknown dtype, pairing or
  * inverse, overlap), TIDE_ERR_HIP.
  */

@@ -176,6 +176,7 @@ To bits_of(From v) {
 #define __syncthreads() lanes::barrier()
 #define __ballot(v) lanes::ballot((v) != 0)
 #define __shfl_xor(v, mask, width) lanes::shuffle_xor(v, mask)
+#define __umulhi(a, b) uint32_t(uint64_t(uint32_t(a)) * uint32_t(b) >> 32)
 #define __ffsll(v) __builtin_ffsll(v)
 #define __clzll(v) __builtin_clzll(v)
 #define __uint_as_float(v) lanes::bits_of<float>(uint32_t(v))

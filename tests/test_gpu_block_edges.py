@@ -1,11 +1,12 @@
 """The block operators on the GPU where a row's vectors meet between waves, and far from zero; as in the tests of their
 numerics, tolerances are error bounds of the formulas."""
+import numpy as np
 import pytest
 import torch
 
-from all_gather_placement_amd import expert_combine_bwd, expert_sort
+from all_gather_placement_amd import expert_combine_bwd, expert_sort, rotary, rotary_bwd, rotary_freqs
 from test_gpu_block import framed, make_ids, untouched
-from test_gpu_step import BF16, FP32, say, whole
+from test_gpu_step import BF16, FP32, U, normal, say, uo, whole, within
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,29 @@ def test_gradients_in_place_where_the_last_vectors_are_two_waves(gpu_available, 
         rows.copy_(x)
         got = expert_combine_bwd(dy, rows, w, sort, drows=rows)
         assert torch.equal(got[1], dw) and torch.equal(rows, drows) and untouched(buf, rows)
+
+
+@pytest.mark.parametrize("kind", [torch.int64, FP32], ids=str)
+@pytest.mark.parametrize("pairing", ["halves", "neighbours"])
+@pytest.mark.parametrize("dtype", [FP32, BF16], ids=str)
+def test_rotary_of_far_positions(gpu_available, dtype, pairing, kind):
+    """Positions up to 2^62: sine and cosine of the angle in 64 bits, off by their rounding to fp32 (2^-25 of a number
+    up to 1) and 2^-35 before it, however far the position is."""
+    say("far positions", dtype, pairing, kind)
+    exponents = np.arange(63)
+    far = np.concatenate([sign * (1 << exponents) + odd for sign in (-1, 1) for odd in (-1, 0, 1)])
+    positions = torch.from_numpy(far)[None].to(kind)
+    freqs = rotary_freqs((9,), base=1000.0)
+    x = normal((positions.shape[1], 2, 18), dtype, 1)
+    a = positions.double().numpy()[0][:, None] * freqs.cpu().numpy()
+    c, s = (torch.from_numpy(f(a))[:, None] for f in (np.cos, np.sin))
+    u, v = (x[..., :9], x[..., 9:]) if pairing == "halves" else (x[..., 0::2], x[..., 1::2])
+    u, v = u.cpu().double(), v.cpu().double()
+    off = (2.0 ** -25 + 2.0 ** -35) * (u.abs() + v.abs())
+    for call, sign in ((rotary, 1), (rotary_bwd, -1)):
+        got = call(x, positions.cuda(), freqs, (9,), pairing).cpu()
+        for g, want, size in zip((got[..., :9], got[..., 9:]) if pairing == "halves" else (got[..., 0::2], got[..., 1::2]),
+                                 (u * c - sign * v * s, v * c + sign * u * s),
+                                 ((u * c).abs() + (v * s).abs(), (v * c).abs() + (u * s).abs())):
+            tol = off + 2 * U * (size + off)  # two products and a sum in fp32
+            within(g, want, tol + uo(dtype) * (want.abs() + tol) + 1e-44, call.__name__)
