@@ -78,6 +78,13 @@ __device__ __forceinline__ void turn(double angle, float* cos, float* sin) {
   *sin = q & 2 ? -v : v;
 }
 
+// A pair turned.  Which products are rounded is written out: lanes whose vectors overlap turn the same pair as different
+// elements of theirs, and have to write the same values.
+__device__ __forceinline__ void turn_pair(float u, float v, float cos, float sin, float* first, float* second) {
+  *first = fmaf(u, cos, -(v * sin));
+  *second = fmaf(u, sin, v * cos);
+}
+
 // A vector, or the two vectors that are turned against each other.
 template <typename T>
 struct Item {
@@ -187,8 +194,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         const float x = item[j].first.get(k), y = item[j].second.get(k);
-        f[k] = x * c[k] - y * s[k];
-        f2[k] = y * c[k] + x * s[k];
+        turn_pair(x, y, c[k], s[k], &f[k], &f2[k]);
       }
       store_part<T, kTiny, kWhole>(item[j].to + p, a.pairs - p, f);
       store_part<T, kTiny, kWhole>(item[j].to + a.pairs + p, a.pairs - p, f2);
@@ -197,8 +203,7 @@ __global__ __launch_bounds__(kMaxThreads) void rotary_kernel(RotaryArgs a, Rotar
 #pragma unroll
       for (int k = 0; k < A; ++k) {
         const float x = item[j].first.get(2 * k), y = item[j].first.get(2 * k + 1);
-        f[2 * k] = x * c[k] - y * s[k];
-        f[2 * k + 1] = y * c[k] + x * s[k];
+        turn_pair(x, y, c[k], s[k], &f[2 * k], &f[2 * k + 1]);
       }
       store_part<T, kTiny, kWhole>(item[j].to + 2 * p, turned - 2 * p, f);
     }

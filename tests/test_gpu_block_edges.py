@@ -58,3 +58,26 @@ def test_rotary_of_far_positions(gpu_available, dtype, pairing, kind):
                                  ((u * c).abs() + (v * s).abs(), (v * c).abs() + (u * s).abs())):
             tol = off + 2 * U * (size + off)  # two products and a sum in fp32
             within(g, want, tol + uo(dtype) * (want.abs() + tol) + 1e-44, call.__name__)
+
+
+@pytest.mark.parametrize("pairing", ["halves", "neighbours"])
+@pytest.mark.parametrize("dtype", [FP32, BF16], ids=str)
+def test_a_pair_is_turned_the_same_wherever_it_lies(gpu_available, dtype, pairing):
+    """Bit for bit: in vectors that overlap, in whole ones, and alone."""
+    say("pairs", dtype, pairing)
+    positions, freqs = torch.arange(3000, device="cuda")[None] * 7, rotary_freqs((128,))
+    u, v = normal((2, 3000, 3, 128), dtype, 1)
+
+    def turned(first, pairs, dim):
+        x = normal((3000, 3, dim), dtype, 2)
+        at = torch.arange(pairs, device="cuda")
+        one, two = (at, pairs + at) if pairing == "halves" else (2 * at, 2 * at + 1)
+        x[..., one], x[..., two] = u[..., first:first + pairs], v[..., first:first + pairs]
+        got = rotary(x, positions, freqs[first:first + pairs].contiguous(), (pairs,), pairing)
+        return torch.stack([got[..., one], got[..., two]])
+
+    want = turned(0, 128, 256)
+    for first, pairs, dim in ((0, 39, 90), (40, 39, 78), (3, 21, 59), (100, 26, 52), (5, 63, 126), (90, 9, 18), (7, 2, 6)):
+        assert torch.equal(turned(first, pairs, dim), want[..., first:first + pairs]), (first, pairs, dim)
+    for first in (0, 1, 2, 3, 4, 5, 6, 7, 127):
+        assert torch.equal(turned(first, 1, 2), want[..., first:first + 1]), first
