@@ -29,7 +29,8 @@ constexpr int kMaxThreads = 512;
 static_assert(TIDE_ROTARY_MAX_DIM / 4 + 2 <= kMaxThreads, "a workgroup takes at least one head, whose parts may end in vectors");
 constexpr int kAngleBytes = 32768;  // of LDS
 
-// Quotients by a number that is known before the launch, of numbers below 2^31.
+// Quotients by a number that is known before the launch, of numbers below 2^31, by a product with its reciprocal rounded
+// up (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994).
 struct Divisor {
   uint32_t d, factor, shift;
   explicit Divisor(uint32_t by) : d(by), factor(0), shift(0) {
