@@ -30,13 +30,16 @@ constexpr int kThreads = 256;
 // Each wave of a workgroup counts its own pairs of each expert: as many waves as 32 KiB of LDS hold the
 // counts of.
 constexpr int kCountBytes = 32768;
-// Of a lane at a time: the code for each is long, and more of it takes longer than it saves (524288 pairs 13.0 us, with 8
-// ids 13.4; 4096 pairs 8.4 and 9.2; 524288 of 2048 experts, many rounds, 72 and 65).
-constexpr int kIds = 2;
+constexpr int kWaves = 16;
+// Ids of a lane at a time: the code for each is long, so that a wave of few rounds does best with few of them, and one
+// of many, where more than 512 experts leave a workgroup fewer waves, with more (in a graph, with 2, 4 and 8: 524288 pairs of
+// 128 experts 13.0 us, 13.0, 13.1; of 512 18.0, 17.7, 18.0; of 1024 28.7, 27.5, 27.1; of 2048 72.8, 67.5, 64.8).  In registers 2 do
+// best (4: 524288 pairs of 128 experts 13.5, 4096 9.1 instead of 8.4).
+constexpr int kHeldIds = 2, kIds = 4, kLongIds = 8;
 constexpr int kExpertBits = 11;
 static_assert(TIDE_MAX_EXPERTS <= 1 << kExpertBits, "bits of an expert's number");
 inline int sort_waves(int experts) {
-  int w = 16;
+  int w = kWaves;
   while (w > 1 && w * experts * 4 > kCountBytes) w /= 2;
   return w;
 }
@@ -97,9 +100,10 @@ __device__ __forceinline__ uint64_t same_expert(int e, int bits) {
   return uint64_t(high) << 32 | low;
 }
 
-// kHeld: a lane's ids stay in registers, with the number of pairs of the same expert that the wave has before each.
-// Otherwise they are read twice, and ranks are found when the wave's first row of each expert is known.
-template <typename I, bool kHeld>
+// A lane takes kAtOnce ids at a time.  kHeld: these are all of them, and stay in registers with the number of pairs of the same
+// expert that the wave has before each.  Otherwise they are read twice, and ranks are found when the wave's first row of
+// each expert is known.
+template <typename I, int kAtOnce, bool kHeld>
 __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, SortShape g) {
   extern __shared__ int lds[];
   const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -112,15 +116,15 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
   const int64_t end = g.begin(a.pairs, blockIdx.x + 1), first = g.begin(a.pairs, blockIdx.x) + wave * int64_t(g.share);
   const int n = int(first + g.share < end ? g.share : end > first ? end - first : 0);
   const I* ids = static_cast<const I*>(a.ids) + first;
-  I id[kIds];
-  int mine[kIds], rank[kIds];
+  I id[kAtOnce];
+  int mine[kAtOnce], rank[kAtOnce];
   const auto load = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < kIds; ++j) id[j] = i0 + j * 64 + lane < n ? ids[i0 + j * 64 + lane] : I(-1);
+    for (int j = 0; j < kAtOnce; ++j) id[j] = i0 + j * 64 + lane < n ? ids[i0 + j * 64 + lane] : I(-1);
   };
   const auto find = [&] {
 #pragma unroll
-    for (int j = 0; j < kIds; ++j) mine[j] = expert_of(id[j], experts);
+    for (int j = 0; j < kAtOnce; ++j) mine[j] = expert_of(id[j], experts);
   };
   load(0);  // while the counts are read
   for (int i = threadIdx.x; i < (waves + 2) * experts; i += blockDim.x) count[i] = 0;
@@ -168,18 +172,18 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
   };
   if constexpr (kHeld) {
 #pragma unroll
-    for (int j = 0; j < kIds; ++j) {
+    for (int j = 0; j < kAtOnce; ++j) {
       if (j * 64 >= n) break;
       rank[j] = take(mine[j]);
     }
   } else {
-    for (int i0 = 0; i0 < n; i0 += 64 * kIds) {
+    for (int i0 = 0; i0 < n; i0 += 64 * kAtOnce) {
       if (i0 > 0) {
         load(i0);
         find();
       }
 #pragma unroll
-      for (int j = 0; j < kIds; ++j)
+      for (int j = 0; j < kAtOnce; ++j)
         if (mine[j] >= 0) atomicAdd(own + mine[j], 1);
     }
   }
@@ -222,13 +226,13 @@ __global__ __launch_bounds__(1024) void expert_place_kernel(ExpertSortArgs a, So
     }
   }
   __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += 64 * kIds) {
+  for (int i0 = 0; i0 < n; i0 += 64 * kAtOnce) {
     if (!kHeld) {
       load(i0);
       find();
     }
 #pragma unroll
-    for (int j = 0; j < kIds; ++j) {
+    for (int j = 0; j < kAtOnce; ++j) {
       if (i0 + j * 64 >= n) break;
       const int i = i0 + j * 64 + lane, e = mine[j];
       int row = -1;
@@ -522,8 +526,10 @@ int sort(const ExpertSortArgs& a, hipStream_t s) {
   if (parts > 1)
     if (const int e = launch(expert_count_kernel<I>, unsigned(parts), 1024, size_t(a.experts) * 4, s, a, g)) return e;
   const size_t lds = (size_t(waves + 3) * a.experts + 1 + waves) * 4;
-  return launch(g.share <= 64 * kIds ? expert_place_kernel<I, true> : expert_place_kernel<I, false>, unsigned(parts),
-                waves * 64, lds, s, a, g);
+  const auto place = g.share <= 64 * kHeldIds ? expert_place_kernel<I, kHeldIds, true>
+                     : waves < kWaves         ? expert_place_kernel<I, kLongIds, false>
+                                              : expert_place_kernel<I, kIds, false>;
+  return launch(place, unsigned(parts), waves * 64, lds, s, a, g);
 }
 
 template <typename F>
