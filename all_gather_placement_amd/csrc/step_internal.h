@@ -153,11 +153,15 @@ int launch_embedding_bwd(const EmbeddingBwdArgs& a, int dtype, int ids_dtype, vo
 
 // The sort cuts the pairs into parts, one for each workgroup; the first launch counts each part's pairs
 // of every expert, the second places them.
-constexpr int kExpertOnePart = 4096;         // pairs that one workgroup sorts, in one launch (8.4 us; two launches 10.8)
-constexpr int kExpertMinPart = 1024;         // of several parts (65536 pairs: 8.4 us; parts of 4096 12.2)
-constexpr int kExpertMaxParts = 256;         // as many as there are compute units (524288 pairs: 13.0 us; 128 parts 13.8)
+// Times are of the call in a graph unless stated, of 128 experts unless stated.
+constexpr int kExpertOnePart = 4096;         // pairs that one workgroup sorts, in one launch (8.3 us, and 8.1 by calls one after
+                                             // another, which two launches make 9.0 to 10.5, though they take 7.9 in a graph)
+constexpr int kExpertMinPart = 1024;         // of several parts (65536 pairs: 8.4 us; parts of 4096 11.2)
+constexpr int kExpertMaxParts = 256;         // as many as there are compute units (1600000 pairs: 20.9 us; 128 parts 25.2, 512
+                                             // 24.6; 524288 pairs: 13.0, 13.0, 17.7)
 constexpr int kExpertMaxCounts = 1 << 16;    // parts * experts, all of which each workgroup reads (524288 pairs of 512
-                                             // experts: 128 parts 18 us, 256 23; of 2048: 32 parts 72, 256 133)
+                                             // experts: 128 parts 17.6 us, 256 20.6; 65536 of 2048: 32 parts 30.8, 64 40.7, though
+                                             // 524288 take 57.7 instead of 64.5 there)
 inline int expert_parts(int64_t pairs, int experts) {
   if (pairs <= kExpertOnePart) return 1;
   const int64_t most = kExpertMaxCounts / experts < kExpertMaxParts ? kExpertMaxCounts / experts : kExpertMaxParts;

@@ -20,8 +20,8 @@ namespace {
 template <bool kHalves>
 constexpr int kItems = kHalves ? 2 : 4;
 // A thread has fewer items where it would make more than four angles for them, which all wait for each other (100000
-// tokens of one head of 64 bf16 11.6 us instead of 13.9), and where there would be few workgroups (512 tokens of 32
-// heads of 128 3.6 us instead of 4.1).
+// tokens of one head of 64 bf16 13.0 us instead of 15.3), and where there would be few workgroups (512 tokens of 32
+// heads of 128 3.7 us instead of 4.1).
 template <typename T, bool kHalves>
 constexpr int kAnglesOf = kHalves ? kVec<T> : kVec<T> / 2;  // of an item
 constexpr int64_t kFewThreads = 512 * 256;
